@@ -23,12 +23,15 @@ __all__ = [
     "lora_apply_multi", "lora_apply_multi_static", "make_pool_struct", "Workspace", "OP_BGMV", "OP_SGMV_SHRINK", "OP_SGMV_EXPAND",
     "OP_APPLY_MULTI", "OP_ROUTE", "OP_MERGE", "OP_LINEAR", "OP_APPLY_PROJ", "STATUS", "lora_merge", "lora_linear_sgmv",
     "PoolManager", "lora_test_stall",
+    "lora_quant_i8", "lora_linear_i8", "lora_linear_i8_sgmv", "lora_rope", "lora_rope_freqs",
+    "OP_LINEAR_I8", "OP_LINEAR_I8_SGMV",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIBNAME = "liblora_sgmv.so"
 
 OP_BGMV, OP_SGMV_SHRINK, OP_SGMV_EXPAND, OP_APPLY_MULTI, OP_ROUTE, OP_MERGE, OP_LINEAR, OP_APPLY_PROJ = range(8)
+OP_LINEAR_I8, OP_LINEAR_I8_SGMV = 8, 9
 STATUS = {0: "LORA_OK", 1: "LORA_ERR_INVALID_ARG", 2: "LORA_ERR_UNSUPPORTED", 4: "LORA_ERR_BAD_ADAPTER",
           8: "LORA_ERR_BAD_SEGMENT", 16: "LORA_ERR_CUDA", 32: "LORA_ERR_WORKSPACE", 64: "LORA_ERR_TIMEOUT"}
 MAX_ADS_PER_REQ = 8
@@ -46,6 +49,11 @@ class LoraPoolStruct(ctypes.Structure):
                 ("B_off", ctypes.c_void_p), ("rank", ctypes.c_void_p), ("A_elems", ctypes.c_int64),
                 ("B_elems", ctypes.c_int64), ("n_adapters", ctypes.c_int32), ("d_in", ctypes.c_int32),
                 ("d_out", ctypes.c_int32), ("max_rank", ctypes.c_int32)]
+
+
+class LoraRopeMat(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64),
+                ("y_token", ctypes.c_int64), ("y_head", ctypes.c_int64), ("heads", ctypes.c_int32)]
 
 
 _lib = None
@@ -102,6 +110,17 @@ def load():
         lib.lora_apply_multi_static.argtypes = [P, i64, P, i64, PP, P, P, P, P, i32, i32, i32, P, P]
         lib.lora_merge.restype = ctypes.c_int
         lib.lora_merge.argtypes = [P, i64, PP, i32, f32, P, sz, P]
+        f64 = ctypes.c_double
+        lib.lora_quant_i8.restype = ctypes.c_int
+        lib.lora_quant_i8.argtypes = [P, i32, i64, P, i64, P, i32, i32, P]
+        lib.lora_linear_i8.restype = ctypes.c_int
+        lib.lora_linear_i8.argtypes = [P, i64, P, P, i64, P, P, i32, i64, i32, i32, i32, P, sz, P]
+        lib.lora_linear_i8_sgmv.restype = ctypes.c_int
+        lib.lora_linear_i8_sgmv.argtypes = [P, i64, P, P, i64, P, i64, P, P, i64, PP, P, P, i32, i32, f32, P, sz, P]
+        lib.lora_rope.restype = ctypes.c_int
+        lib.lora_rope.argtypes = [ctypes.POINTER(LoraRopeMat), i32, i32, P, i32, P, i32, i32, i32, i32, i32, f32, P]
+        lib.lora_rope_freqs.restype = ctypes.c_int
+        lib.lora_rope_freqs.argtypes = [i32, i32, f64, f64, f64, f64, f64, P, P]
         lib.lora_pm_create.restype = ctypes.c_int
         lib.lora_pm_create.argtypes = [PP, P, ctypes.POINTER(ctypes.c_void_p)]
         lib.lora_pm_destroy.restype = None
@@ -368,6 +387,183 @@ def lora_linear_sgmv(X, W, Y, pool, seg_off, seg_ad, scale: float, ws: Workspace
                              _ptr(seg_ad), n_seg, N, float(scale), ws.ptr(), ws.nbytes, _stream_ptr(stream)),
         "lora_linear_sgmv")
     return ws
+
+
+_DTYPES = {"torch.bfloat16": 0, "torch.float16": 1, "torch.float32": 2}      # lora_dtype
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+
+
+def _dtype(t, name: str) -> int:
+    code = _DTYPES.get(str(t.dtype))
+    if code is None:
+        raise LoraError(f"{name} must be bf16, fp16 or fp32", 2)
+    return code
+
+
+def _rows(t, name: str, dtypes=None):
+    """Leading dimension of a 2-D tensor of rows (a single row has none: any that fits will do)."""
+    if t.dim() != 2 or (dtypes and str(t.dtype) not in dtypes) or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise LoraError(f"{name} must be a 2-D tensor with unit-stride columns", 1)
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def _vec(t, n: int, name: str):
+    if str(t.dtype) != "torch.float32" or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise LoraError(f"{name} must be a contiguous fp32 tensor of {n} scales", 1)
+
+
+class _Launch:
+    """The stream of a call and, where the tensors live on another device than the current
+    one, that device made current for its duration (a launch goes to the current device)."""
+
+    def __init__(self, stream, *tensors):
+        torch = _torch()
+        _check_dev(*tensors)
+        dev = tensors[0].device
+        if any(t.device != dev for t in tensors):
+            raise LoraError("tensors must live on one CUDA device", 1)
+        self.device = dev
+        self._guard = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+        self._given = stream
+        self.stream = int((stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+        return False
+
+    def workspace(self, nbytes: int) -> Workspace:
+        """A workspace of this device and stream: calls on two streams never share one.  Under
+        graph capture it is a fresh one from the graph's memory, so that no two graphs share it."""
+        torch = _torch()
+        if self._given is not None:                    # allocated, and freed, in that stream's order
+            with torch.cuda.stream(self._given):
+                return self._workspace(nbytes)
+        return self._workspace(nbytes)
+
+    def _workspace(self, nbytes: int) -> Workspace:
+        if _torch().cuda.is_current_stream_capturing():
+            return Workspace(nbytes, device=self.device)
+        key = (self.device.index, self.stream)
+        ws = _stream_ws.get(key)
+        if ws is None or ws.nbytes < nbytes:
+            ws = _stream_ws[key] = Workspace(max(nbytes, 2 * (ws.nbytes if ws else 0)), device=self.device)
+        return ws
+
+
+_stream_ws: dict = {}
+
+
+def lora_quant_i8(X, Q, S, stream=None):
+    """Q[n] = round(127 X[n] / max|X[n]|) (int8), S[n] = max|X[n]| / 127 for rows of bf16, fp16 or fp32."""
+    lib = load()
+    with _Launch(stream, X, Q, S) as la:
+        ldx, ldq = _rows(X, "X"), _rows(Q, "Q", ("torch.int8",))
+        if tuple(Q.shape) != tuple(X.shape):
+            raise LoraError("Q must have X's shape", 1)
+        _vec(S, X.shape[0], "S")
+        _rc(lib.lora_quant_i8(_ptr(X), _dtype(X, "X"), ldx, _ptr(Q), ldq, _ptr(S), int(X.shape[0]),
+                              int(X.shape[1]), la.stream), "lora_quant_i8")
+
+
+def _i8_operands(Q, Sx, Wq, Sw, Y):
+    ldq, ldw = _rows(Q, "Q", ("torch.int8",)), _rows(Wq, "Wq", ("torch.int8",))
+    ldy = _rows(Y, "Y")
+    N, d_in, d_out = int(Q.shape[0]), int(Q.shape[1]), int(Wq.shape[0])
+    if int(Wq.shape[1]) != d_in or tuple(Y.shape) != (N, d_out):
+        raise LoraError("Q [N, d_in], Wq [d_out, d_in] and Y [N, d_out] do not fit together", 1)
+    _vec(Sx, N, "Sx")
+    _vec(Sw, d_out, "Sw")
+    return ldq, ldw, ldy, N, d_in, d_out
+
+
+def lora_linear_i8(Q, Sx, Wq, Sw, Y, ws: Workspace | None = None, stream=None):
+    """Y[n][o] = Sx[n] Sw[o] sum_i Q[n][i] Wq[o][i] for int8 tokens and weight; Y is bf16, fp16 or
+    fp32 and overwritten.  Returns the workspace (its error word: lora_get_error)."""
+    lib = load()
+    with _Launch(stream, Q, Sx, Wq, Sw, Y) as la:
+        ldq, ldw, ldy, N, d_in, d_out = _i8_operands(Q, Sx, Wq, Sw, Y)
+        ws = ws or la.workspace(256)
+        _rc(lib.lora_linear_i8(_ptr(Q), ldq, _ptr(Sx), _ptr(Wq), ldw, _ptr(Sw), _ptr(Y), _dtype(Y, "Y"), ldy, N,
+                               d_in, d_out, ws.ptr(), ws.nbytes, la.stream), "lora_linear_i8")
+    return ws
+
+
+def lora_linear_i8_sgmv(Q, Sx, X, Wq, Sw, Y, pool, seg_off, seg_ad, scale: float, ws: Workspace | None = None,
+                        stream=None, max_rank: int | None = None):
+    """lora_linear_i8 plus scale * B[a] A[a] X[n] for rows of segment k (a = seg_ad[k]; -1: none).
+
+    X holds the bf16 tokens that Q and Sx are the 8-bit form of; Y is bf16, overwritten inside
+    the segments and left alone outside them."""
+    lib = load()
+    torch = _torch()
+    with _Launch(stream, Q, Sx, X, Wq, Sw, Y, seg_off, seg_ad, pool.A, pool.B) as la:
+        ldq, ldw, ldy, N, d_in, d_out = _i8_operands(Q, Sx, Wq, Sw, Y)
+        ps = make_pool_struct(pool, max_rank)
+        _mat(Y, ps.d_out, "Y")
+        ldx = _mat(X, ps.d_in, "X")
+        if d_in != ps.d_in or int(X.shape[0]) != N:
+            raise LoraError("Q, X and the pool disagree on N or d_in", 1)
+        n_seg = int(seg_ad.numel())
+        for t, n, name in ((seg_off, n_seg + 1, "seg_off"), (seg_ad, n_seg, "seg_ad")):
+            if t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous():
+                raise LoraError(f"{name} must be a contiguous int32 tensor of {n} entries", 1)
+        need = lora_workspace_size(OP_LINEAR_I8_SGMV, N, ps.n_adapters, ps.d_in, ps.d_out, ps.max_rank, n_seg)
+        ws = ws or la.workspace(need)
+        _rc(lib.lora_linear_i8_sgmv(_ptr(Q), ldq, _ptr(Sx), _ptr(X), ldx, _ptr(Wq), ldw, _ptr(Sw), _ptr(Y), ldy,
+                                    ctypes.byref(ps), _ptr(seg_off), _ptr(seg_ad), n_seg, N, float(scale),
+                                    ws.ptr(), ws.nbytes, la.stream), "lora_linear_i8_sgmv")
+    return ws
+
+
+def lora_rope(xs, ys, pos, freqs, interleaved: bool = False, mscale: float = 1.0, inverse: bool = False,
+              stream=None):
+    """Rotary positions on up to four tensors [N, heads, dim] that share their tokens (q and k).
+
+    ys[i] receives xs[i] rotated by pos * freqs (ys[i] may be xs[i] itself: in place).  freqs: fp64
+    [rot / 2] on the device, rot <= dim; pos: int32 or int64 [N].  `inverse` turns back: the gradient."""
+    lib = load()
+    torch = _torch()
+    xs, ys = list(xs), list(ys)
+    if not xs or len(xs) != len(ys):
+        raise LoraError("one output per input", 1)
+    with _Launch(stream, *xs, *ys, pos, freqs) as la:
+        n, dim = (int(xs[0].shape[0]), int(xs[0].shape[2])) if xs[0].dim() == 3 else (0, 0)
+        for x, y in zip(xs, ys):
+            if (x.dim() != 3 or x.shape != y.shape or x.dtype != y.dtype or x.dtype != xs[0].dtype or
+                    int(x.shape[0]) != n or int(x.shape[2]) != dim or x.stride(2) != 1 or y.stride(2) != 1):
+                raise LoraError("tensors [N, heads, dim] of one type, N and dim, unit stride inside a head", 1)
+        if pos.dtype not in (torch.int32, torch.int64) or pos.dim() != 1 or int(pos.shape[0]) != n or (
+                n > 1 and pos.stride(0) != 1):
+            raise LoraError("pos must be a contiguous int32 or int64 tensor [N]", 1)
+        if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+            raise LoraError("freqs must be a contiguous fp64 tensor [rot / 2]", 1)
+        mats = (LoraRopeMat * len(xs))(*[
+            LoraRopeMat(_ptr(x), _ptr(y), x.stride(0), x.stride(1), y.stride(0), y.stride(1), int(x.shape[1]))
+            for x, y in zip(xs, ys)])
+        _rc(lib.lora_rope(mats, len(xs), _dtype(xs[0], "x"), _ptr(pos), pos.element_size(), _ptr(freqs), n, dim,
+                          2 * int(freqs.numel()), int(bool(interleaved)), int(bool(inverse)), float(mscale),
+                          la.stream), "lora_rope")
+
+
+def lora_rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, low: float = 1.0,
+                    high: float = 32.0, original: float = 0.0):
+    """(freqs, mscale) for lora_rope: fp64 CPU tensor [rot / 2] in radians per position, and the
+    factor on the rotated values.  scaling: 'none', 'linear', 'ntk', 'bands' or 'yarn' (see
+    lora_rope_freqs in the header for each form and for low, high and original)."""
+    torch = _torch()
+    if scaling not in _ROPE_SCALINGS:
+        raise LoraError(f"unknown scaling {scaling!r}", 2)
+    out = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64)
+    m = ctypes.c_double(0.0)
+    _rc(load().lora_rope_freqs(_ROPE_SCALINGS[scaling], int(rot), float(base), float(factor), float(low), float(high),
+                               float(original), out.data_ptr(), ctypes.addressof(m)), "lora_rope_freqs")
+    return out, float(m.value)
 
 
 def lora_sgmv_expand(V, Y, pool, seg_off, seg_ad, scale: float, ws: Workspace | None = None,

@@ -121,7 +121,7 @@ bool layout(int op, int32_t N, int32_t n_adapters, int32_t d_in, int32_t max_ran
         v = (size_t)N * max_ads * max_rank * 4;
     else if (op == LORA_OP_APPLY_PROJ)
         v = (size_t)N * max_rank * 4;       // V of all the projections side by side
-    else if (op == LORA_OP_LINEAR) {
+    else if (op == LORA_OP_LINEAR || op == LORA_OP_LINEAR_I8_SGMV) {
         L->kv = (max_rank + 63) & ~63;
         v = (size_t)N * 2 * L->kv * 2;      // s V, bf16 high and low parts
     }
@@ -162,6 +162,18 @@ lora_status check_ws(void *ws, size_t ws_bytes, const Layout &L)
 {
     if (!ws || misaligned(ws, kAlign) || ws_bytes < L.total)
         return LORA_ERR_WORKSPACE;
+    return LORA_OK;
+}
+
+// The 8-bit operands of a projection: rows and addresses on 16-byte boundaries.
+lora_status check_i8(const int8_t *Q, int64_t ldq, const float *Sx, const int8_t *W, int64_t ldw, const float *Sw,
+                     int32_t N, int32_t d_in, int32_t d_out)
+{
+    if (N < 0 || d_in <= 0 || d_out <= 0 || (N > 0 && (!Q || !Sx)) || !W || !Sw || ldq < d_in || ldw < d_in)
+        return LORA_ERR_INVALID_ARG;
+    if (d_in > LORA_MAX_I8_IN || (d_in & 7) || (d_out & 7) || (ldq & 15) || (ldw & 15) || misaligned(Q, 16) ||
+        misaligned(W, 16) || misaligned(Sx, 4) || misaligned(Sw, 4))
+        return LORA_ERR_UNSUPPORTED;
     return LORA_OK;
 }
 
@@ -306,7 +318,11 @@ size_t lora_workspace_size(int op, int32_t N, int32_t n_adapters, int32_t d_in, 
     if (op == LORA_OP_MERGE)
         return n_adapters >= 1 && n_adapters <= LORA_MAX_ADAPTERS && N == d_out
                    ? merge_workspace_size(d_in, d_out, max_rank) : 0;
-    if (op < LORA_OP_BGMV || op > LORA_OP_APPLY_PROJ || op == LORA_OP_MERGE)
+    if (op == LORA_OP_LINEAR_I8)
+        return N >= 0 && d_in > 0 && d_in <= LORA_MAX_I8_IN && d_out > 0 ? sizeof(WsHeader) : 0;
+    if (op < LORA_OP_BGMV || op > LORA_OP_LINEAR_I8_SGMV || op == LORA_OP_MERGE)
+        return 0;
+    if (op == LORA_OP_LINEAR_I8_SGMV && d_in > LORA_MAX_I8_IN)
         return 0;
     Layout L;
     if (!layout(op, N, n_adapters, d_in, max_rank, n_items, max_ads_per_req, &L))
@@ -316,6 +332,8 @@ size_t lora_workspace_size(int op, int32_t N, int32_t n_adapters, int32_t d_in, 
 
 int lora_kernel_launches(int op, int32_t N, int32_t n_adapters, int32_t d_in, int32_t n_items)
 {
+    if (op == LORA_OP_LINEAR_I8)
+        return N > 0 && d_in > 0 && d_in <= LORA_MAX_I8_IN ? 1 : 0;
     if (N <= 0 || n_adapters < 1 || n_adapters > LORA_MAX_ADAPTERS || d_in <= 0)
         return 0;
     switch (op) {
@@ -331,6 +349,7 @@ int lora_kernel_launches(int op, int32_t N, int32_t n_adapters, int32_t d_in, in
     case LORA_OP_MERGE:   // preparation + expand (tensor cores), or + plan + expand
         return tc_enabled() && N >= kTcGroup ? 2 : 3;
     case LORA_OP_LINEAR:  // plan + shrink + projection
+    case LORA_OP_LINEAR_I8_SGMV:
         return n_items > 0 ? 3 : 0;
     default:
         return 0;
@@ -750,6 +769,114 @@ lora_status lora_linear_sgmv(const void *X, int64_t ldx, const void *W, int64_t 
     const int64_t n_ns = (pool->d_out + 255) / 256;
     const int64_t max_units = (int64_t)max_tiles * n_ns;
     LORA_CUDA(launch_tc_linear(la, (int)(max_units < (1 << 30) ? max_units : (1 << 30)), s));
+    return LORA_OK;
+}
+
+lora_status lora_linear_i8(const int8_t *Q, int64_t ldq, const float *Sx, const int8_t *Wq, int64_t ldw,
+                           const float *Sw, void *Y, int32_t dtype, int64_t ldy, int32_t N, int32_t d_in,
+                           int32_t d_out, void *ws, size_t ws_bytes, void *stream)
+{
+    LORA_TRY(check_i8(Q, ldq, Sx, Wq, ldw, Sw, N, d_in, d_out));
+    if (dtype < LORA_BF16 || dtype > LORA_F32)
+        return LORA_ERR_UNSUPPORTED;
+    LORA_TRY(check_mat(Y, ldy, d_out, N));
+    if (!ws || misaligned(ws, kAlign) || ws_bytes < sizeof(WsHeader))
+        return LORA_ERR_WORKSPACE;
+    if (N == 0)
+        return LORA_OK;
+    I8Args a = {};
+    a.Q = Q;
+    a.ldq = ldq;
+    a.Sx = Sx;
+    a.W = Wq;
+    a.ldw = ldw;
+    a.Sw = Sw;
+    a.Y = Y;
+    a.ldy = ldy;
+    a.dtype = dtype;
+    a.N = N;
+    a.d_in = d_in;
+    a.d_out = d_out;
+    a.err = &static_cast<WsHeader *>(ws)->err;
+    LORA_CUDA(launch_linear_i8(a, 0, (cudaStream_t)stream));
+    return LORA_OK;
+}
+
+lora_status lora_linear_i8_sgmv(const int8_t *Q, int64_t ldq, const float *Sx, const void *X, int64_t ldx,
+                                const int8_t *Wq, int64_t ldw, const float *Sw, void *Y, int64_t ldy,
+                                const lora_pool *pool, const int32_t *seg_off, const int32_t *seg_ad,
+                                int32_t n_seg, int32_t N, float scale, void *ws, size_t ws_bytes, void *stream)
+{
+    LORA_TRY(check_pool(pool));
+    if (N < 0 || n_seg < 0 || !seg_off || (n_seg > 0 && !seg_ad))
+        return LORA_ERR_INVALID_ARG;
+    LORA_TRY(check_i8(Q, ldq, Sx, Wq, ldw, Sw, N, pool->d_in, pool->d_out));
+    LORA_TRY(check_mat(X, ldx, pool->d_in, N));
+    LORA_TRY(check_mat(Y, ldy, pool->d_out, N));
+    Layout L;
+    if (!layout(LORA_OP_LINEAR_I8_SGMV, N, pool->n_adapters, pool->d_in, pool->max_rank, n_seg, 1, &L))
+        return LORA_ERR_INVALID_ARG;
+    LORA_TRY(check_ws(ws, ws_bytes, L));
+    if (N == 0 || n_seg == 0)
+        return LORA_OK;
+    if (!tc_enabled())
+        return LORA_ERR_UNSUPPORTED;
+    cudaStream_t s = (cudaStream_t)stream;
+    WsHeader *hdr = at<WsHeader>(ws, L.hdr);
+    Group *groups = at<Group>(ws, L.groups);
+
+    // tiles and s V (bf16 high and low parts) as for lora_linear_sgmv
+    TcArgs ta = {};
+    tc_encode_a(ta, pool->A, pool->A_elems, pool->d_in);
+    if (!tc_encode_x(ta, X, N, pool->d_in, ldx))
+        return LORA_ERR_UNSUPPORTED;
+    PlanArgs pa = {};
+    pa.mode = kModeSgmv;
+    pa.N = N;
+    pa.item_off = seg_off;
+    pa.n_items = n_seg;
+    pa.groups = groups;
+    pa.max_groups = L.max_groups;
+    pa.group = kTcGroup;
+    pa.hdr = hdr;
+    LORA_CUDA(launch_plan(pa, s));
+    ta.mode = kModeSgmv;
+    ta.groups = groups;
+    ta.hdr = hdr;
+    ta.seg_ad = seg_ad;
+    ta.max_ads = 1;
+    ta.scale = scale;
+    ta.pool = pool_dev(pool);
+    ta.Vb = at<__nv_bfloat16>(ws, L.V);
+    ta.ldvb = 2 * (int64_t)L.kv;
+    ta.vb_lo = L.kv;
+    ta.allow_none = 1;
+    ta.err = &hdr->err;
+    const int max_tiles = N / kTcGroup + n_seg + 1;
+    LORA_CUDA(launch_tc_shrink(ta, max_tiles, pool->max_rank, s));
+
+    I8Args a = {};
+    a.Q = Q;
+    a.ldq = ldq;
+    a.Sx = Sx;
+    a.W = Wq;
+    a.ldw = ldw;
+    a.Sw = Sw;
+    a.Y = Y;
+    a.ldy = ldy;
+    a.dtype = LORA_BF16;
+    a.N = N;
+    a.d_in = pool->d_in;
+    a.d_out = pool->d_out;
+    a.err = &hdr->err;
+    a.groups = groups;
+    a.hdr = hdr;
+    a.seg_ad = seg_ad;
+    a.pool = pool_dev(pool);
+    a.Vb = ta.Vb;
+    a.ldvb = ta.ldvb;
+    a.kv = L.kv;
+    LORA_CUDA(launch_linear_i8(a, max_tiles, s));
     return LORA_OK;
 }
 

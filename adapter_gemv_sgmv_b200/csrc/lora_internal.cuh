@@ -312,6 +312,31 @@ bool lin_encode(LinArgs &a, const void *X, int64_t ldx, int32_t N, const void *W
                 int64_t ldvb, const void *B, int64_t B_elems, int32_t d_in, int32_t d_out);
 cudaError_t launch_tc_linear(const LinArgs &a, int max_units, cudaStream_t s);
 
+// -------------------------------------- projection with 8-bit operands (+ LoRA)
+struct I8Args {
+    const int8_t *Q;         // [N, d_in], row stride ldq
+    int64_t ldq;
+    const float *Sx;         // [N]
+    const int8_t *W;         // [d_out, d_in], row stride ldw
+    int64_t ldw;
+    const float *Sw;         // [d_out]
+    void *Y;                 // [N, d_out] of dtype
+    int64_t ldy;
+    int32_t dtype;
+    int32_t N, d_in, d_out;
+    uint32_t *err;
+    // segments with adapters (groups == nullptr: every row, no adapter)
+    const Group *groups;     // tiles of <= 128 rows, one segment each
+    const WsHeader *hdr;
+    const int32_t *seg_ad;   // -1: no adapter
+    PoolDev pool;
+    const __nv_bfloat16 *Vb; // s V as bf16 parts [N, 2 kv] (high, then low from column kv)
+    int64_t ldvb;
+    int32_t kv;
+};
+
+cudaError_t launch_linear_i8(const I8Args &a, int max_tiles, cudaStream_t s);
+
 // Workspace bytes of lora_merge (0 for unsupported sizes).
 size_t merge_workspace_size(int32_t d_in, int32_t d_out, int32_t max_rank);
 

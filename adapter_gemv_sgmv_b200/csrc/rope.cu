@@ -1,0 +1,388 @@
+// lora_rope: rotary positions on the heads of projections that share their tokens
+// (q and k right after their adapted projection).  With t = pos[n] * freq[j], the pair
+// (a, b) of a head's first rot dimensions becomes
+//
+//     a' = m (a cos t - b sin t),   b' = m (b cos t + a sin t)
+//
+// (inverse: t -> -t, the transpose, which is the gradient), pair j being dimensions
+// (j, j + rot/2) or, interleaved, (2j, 2j + 1); dimensions past rot are copied.
+//
+// The angle is what needs care: at position 10^6 a frequency of 1 turns 160 000 times,
+// and fp32 would leave an error of several hundredths of a radian.  So the turns
+// u = pos * (freq / 2 pi) are formed and reduced to [-1/2, 1/2] in fp64, and only the
+// reduced angle goes to sincospif in fp32.  cos and sin carry m; the products are fp32,
+// each output is rounded to its type once.
+//
+// Bound: HBM, one read and one write per element.  A block takes one token (several
+// where a token has few heads): its cos / sin come out once, in shared memory, for all
+// heads, and each thread's loads of x are in flight while they are computed.
+
+#include "lora_internal.cuh"
+
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+namespace lora {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeHold = 2;        // items a thread loads ahead of the angles
+
+struct RopeMat {
+    const void *x;
+    void *y;
+    int64_t xs, xh, ys, yh;         // token and head strides, elements
+    int32_t heads;
+    int32_t first;                  // items of a token before this matrix's
+};
+
+struct RopeArgs {
+    RopeMat mat[LORA_MAX_PROJ];
+    int32_t n_mat;
+    const void *pos;
+    int32_t pos64;
+    const double *freq;
+    int32_t N, dim, half;           // half = rot / 2
+    int32_t rot_items, head_items;  // items of a head that rotate; all of them
+    int32_t items;                  // of a token
+    int32_t tokens;                 // per block
+    float m;
+    float sign;                     // -1: inverse
+};
+
+// V elements at p as fp32
+template <class T, int V> __device__ __forceinline__ void get(const T *p, float (&f)[V])
+{
+    if constexpr (V == 1) {
+        f[0] = (float)p[0];
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (std::is_same<T, float>::value) {
+                f[i] = __uint_as_float(w[i]);
+            } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                f[2 * i] = h.x;
+                f[2 * i + 1] = h.y;
+            }
+        }
+    }
+}
+
+template <class T, int V> __device__ __forceinline__ void put(T *p, const float (&f)[V])
+{
+    if constexpr (V == 1) {
+        if constexpr (std::is_same<T, float>::value)
+            p[0] = f[0];
+        else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+            p[0] = __float2bfloat16_rn(f[0]);
+        else
+            p[0] = __float2half_rn(f[0]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (std::is_same<T, float>::value) {
+                w[i] = __float_as_uint(f[i]);
+            } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            } else {
+                const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// An item: V pairs of one head (two runs of V elements; interleaved: one run of V
+// elements, or a single pair where V is 1), or a run of V copied from past rot.
+template <class T, int V, bool INTER> struct Item {
+    static constexpr int U = INTER && V == 1 ? 2 : V;
+    const T *x;
+    T *y;
+    int pair;             // first pair's place in the block's cos / sin; -1: copy
+    float a[U], b[INTER ? 1 : U];
+};
+
+template <class T, int V, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ RopeArgs p)
+{
+    extern __shared__ float2 cs[];                   // [tokens][half]
+    using It = Item<T, V, INTER>;
+    constexpr int U = It::U;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, nt = blockDim.x;
+    const int n0 = blockIdx.x * p.tokens;
+    const int n_tok = min(p.tokens, p.N - n0);
+    const int total = n_tok * p.items;
+
+    auto load = [&](int i, It &it) {
+        const int t = i / p.items;
+        int k = i - t * p.items;
+        int q = 0;
+#pragma unroll
+        for (int j = 1; j < LORA_MAX_PROJ; ++j)
+            if (j < p.n_mat && k >= p.mat[j].first)
+                q = j;
+        k -= p.mat[q].first;
+        const int h = k / p.head_items, c = k - h * p.head_items;
+        const int64_t n = n0 + t;
+        it.x = static_cast<const T *>(p.mat[q].x) + n * p.mat[q].xs + h * p.mat[q].xh;
+        it.y = static_cast<T *>(p.mat[q].y) + n * p.mat[q].ys + h * p.mat[q].yh;
+        if (c < p.rot_items) {
+            const int e = INTER ? c * U : c * V;     // first element
+            it.pair = t * p.half + (INTER ? e / 2 : e);
+            it.x += e;
+            it.y += e;
+            if constexpr (V == 1) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    it.a[u] = (float)it.x[u];
+            } else {
+                get<T, V>(it.x, it.a);
+            }
+            if constexpr (!INTER)
+                get<T, V>(it.x + p.half, it.b);
+        } else {
+            const int e = 2 * p.half + (c - p.rot_items) * V;
+            it.pair = -1;
+            it.x += e;
+            it.y += e;
+            if constexpr (V == 1)
+                it.a[0] = (float)it.x[0];
+            else
+                get<T, V>(it.x, it.a);
+        }
+    };
+    auto store = [&](It &it) {
+        if (it.pair < 0) {
+            if constexpr (V == 1) {
+                float f[1] = {it.a[0]};
+                put<T, 1>(it.y, f);
+            } else {
+                put<T, V>(it.y, it.a);
+            }
+            return;
+        }
+        if constexpr (INTER) {
+            float o[U];
+#pragma unroll
+            for (int u = 0; u < U; u += 2) {
+                const float2 w = cs[it.pair + u / 2];
+                o[u] = it.a[u] * w.x - it.a[u + 1] * w.y;
+                o[u + 1] = it.a[u + 1] * w.x + it.a[u] * w.y;
+            }
+            if constexpr (V == 1) {
+                float f0[1] = {o[0]}, f1[1] = {o[1]};
+                put<T, 1>(it.y, f0);
+                put<T, 1>(it.y + 1, f1);
+            } else {
+                put<T, V>(it.y, o);
+            }
+        } else {
+            float oa[V], ob[V];
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                const float2 w = cs[it.pair + u];
+                oa[u] = it.a[u] * w.x - it.b[u] * w.y;
+                ob[u] = it.b[u] * w.x + it.a[u] * w.y;
+            }
+            put<T, V>(it.y, oa);
+            put<T, V>(it.y + p.half, ob);
+        }
+    };
+
+    It it[kRopeHold];
+#pragma unroll
+    for (int j = 0; j < kRopeHold; ++j)
+        if (tid + j * nt < total)
+            load(tid + j * nt, it[j]);
+    for (int i = tid; i < n_tok * p.half; i += nt) {
+        const int t = i / p.half, j = i - t * p.half;
+        const double at = p.pos64 ? (double)static_cast<const int64_t *>(p.pos)[n0 + t]
+                                  : (double)static_cast<const int32_t *>(p.pos)[n0 + t];
+        // freq / 2 pi is off by 2^-53 of itself, the fma rounds once: at 2^31 positions of
+        // frequency 1 the angle is still within 2^-23
+        const double f = p.freq[j] * 0.15915494309189533577;
+        const double u = fma(at, f, -rint(at * f));
+        float s, c;
+        sincospif(2.f * (float)u, &s, &c);
+        cs[i] = make_float2(c * p.m, s * p.m * p.sign);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kRopeHold; ++j)
+        if (tid + j * nt < total)
+            store(it[j]);
+    for (int i = tid + kRopeHold * nt; i < total; i += nt) {
+        load(i, it[0]);
+        store(it[0]);
+    }
+}
+
+template <class T, bool INTER>
+cudaError_t launch_rope_t(RopeArgs &a, bool vec, bool copy, cudaStream_t s)
+{
+    constexpr int VW = 16 / sizeof(T);
+    const int V = vec ? VW : 1;
+    const int rot = 2 * a.half;
+    a.rot_items = INTER ? (vec ? rot / VW : a.half) : a.half / V;
+    a.head_items = a.rot_items + (copy ? (a.dim - rot) / V : 0);
+    int64_t items = 0;
+    for (int i = 0; i < a.n_mat; ++i) {
+        a.mat[i].first = (int32_t)items;
+        items += (int64_t)a.mat[i].heads * a.head_items;
+    }
+    if (items > (1 << 24))
+        return cudaErrorInvalidValue;
+    a.items = (int32_t)items;
+    a.tokens = 1;
+    while (a.tokens < 8 && a.tokens * items < kRopeThreads / 2)
+        a.tokens *= 2;
+    int threads = kRopeThreads;
+    const int64_t want = (a.tokens * items + kRopeHold - 1) / kRopeHold;
+    while (threads > 64 && threads / 2 >= want)
+        threads /= 2;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.N + a.tokens - 1) / a.tokens);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = sizeof(float2) * a.tokens * a.half;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    return vec ? cudaLaunchKernelEx(&cfg, k_rope<T, VW, INTER>, a) : cudaLaunchKernelEx(&cfg, k_rope<T, 1, INTER>, a);
+}
+
+template <class T> cudaError_t launch_rope(RopeArgs &a, bool inter, bool vec, bool copy, cudaStream_t s)
+{
+    return inter ? launch_rope_t<T, true>(a, vec, copy, s) : launch_rope_t<T, false>(a, vec, copy, s);
+}
+
+}  // namespace
+}  // namespace lora
+
+using namespace lora;
+
+namespace {
+
+// Distinct (token, head) of a tensor lie in distinct elements: tokens hold whole heads
+// apart, or heads hold whole tokens apart.
+bool apart(int64_t token, int64_t head, int32_t N, int32_t heads, int32_t dim)
+{
+    const __int128 t = token, h = head;
+    const bool by_token = (heads == 1 || h >= dim) && (N == 1 || t >= (__int128)(heads - 1) * h + dim);
+    const bool by_head = (N == 1 || t >= dim) && (heads == 1 || h >= (__int128)(N - 1) * t + dim);
+    return by_token || by_head;
+}
+
+}  // namespace
+
+extern "C" lora_status lora_rope(const lora_rope_mat *mats, int32_t n_mats, int32_t dtype, const void *pos,
+                                 int32_t pos_bytes, const double *freq, int32_t N, int32_t dim, int32_t rot,
+                                 int32_t interleaved, int32_t inverse, float mscale, void *stream)
+{
+    if (!mats || n_mats < 1 || N < 0 || dim < 2 || rot < 2 || rot > dim || (rot & 1) || (N > 0 && (!pos || !freq)) ||
+        (pos_bytes != 4 && pos_bytes != 8))
+        return LORA_ERR_INVALID_ARG;
+    if (n_mats > LORA_MAX_PROJ || dim > LORA_MAX_ROPE_DIM || dtype < LORA_BF16 || dtype > LORA_F32)
+        return LORA_ERR_UNSUPPORTED;
+    const int es = dtype == LORA_F32 ? 4 : 2, vw = 16 / es;
+    if (((uintptr_t)pos & (pos_bytes - 1)) || ((uintptr_t)freq & 7))
+        return LORA_ERR_UNSUPPORTED;
+    RopeArgs a = {};
+    // 16-byte access: every run of 16 bytes that an item moves starts on a 16-byte boundary
+    bool vec = (interleaved ? rot % vw == 0 : (rot / 2) % vw == 0) && dim % vw == 0, copy = false;
+    for (int i = 0; i < n_mats; ++i) {
+        const lora_rope_mat &m = mats[i];
+        if (N > 0 && (!m.x || !m.y))
+            return LORA_ERR_INVALID_ARG;
+        if (m.heads < 1 || m.x_token < 0 || m.x_head < 0 || !apart(m.y_token, m.y_head, N, m.heads, dim))
+            return LORA_ERR_INVALID_ARG;
+        const bool same = m.x == m.y;
+        if (same && (m.x_token != m.y_token || m.x_head != m.y_head))
+            return LORA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (N > 0 && mats[j].y == m.y)
+                return LORA_ERR_INVALID_ARG;
+        if (((uintptr_t)m.x | (uintptr_t)m.y) & (es - 1))
+            return LORA_ERR_UNSUPPORTED;
+        copy |= !same && rot < dim;
+        vec &= !((((uintptr_t)m.x | (uintptr_t)m.y) & 15) ||
+                 ((m.x_token | m.x_head | m.y_token | m.y_head) & (vw - 1)));
+        a.mat[i] = {m.x, m.y, m.x_token, m.x_head, m.y_token, m.y_head, m.heads, 0};
+    }
+    int64_t heads = 0;
+    for (int i = 0; i < n_mats; ++i)
+        heads += mats[i].heads;
+    if (heads > LORA_MAX_ROPE_HEADS)
+        return LORA_ERR_UNSUPPORTED;
+    if (N == 0)
+        return LORA_OK;
+    a.n_mat = n_mats;
+    a.pos = pos;
+    a.pos64 = pos_bytes == 8;
+    a.freq = freq;
+    a.N = N;
+    a.dim = dim;
+    a.half = rot / 2;
+    a.m = mscale;
+    a.sign = inverse ? -1.f : 1.f;
+    cudaStream_t s = (cudaStream_t)stream;
+    const bool inter = interleaved != 0;
+    const cudaError_t e = dtype == LORA_BF16 ? launch_rope<__nv_bfloat16>(a, inter, vec, copy, s)
+                        : dtype == LORA_F16 ? launch_rope<__half>(a, inter, vec, copy, s)
+                                            : launch_rope<float>(a, inter, vec, copy, s);
+    return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+}
+
+extern "C" lora_status lora_rope_freqs(int32_t scaling, int32_t rot, double base, double factor, double low,
+                                       double high, double original, double *freq, double *mscale)
+{
+    if (!freq || !mscale || rot < 2 || (rot & 1) || !(base > 1.0) || !std::isfinite(base))
+        return LORA_ERR_INVALID_ARG;
+    if (scaling < LORA_ROPE_NONE || scaling > LORA_ROPE_YARN)
+        return LORA_ERR_UNSUPPORTED;
+    if (scaling != LORA_ROPE_NONE && (!(factor > 0.0) || !std::isfinite(factor)))
+        return LORA_ERR_INVALID_ARG;
+    const bool ramps = scaling == LORA_ROPE_BANDS || scaling == LORA_ROPE_YARN;
+    if (ramps && (!(low > 0.0) || !(high > low) || !std::isfinite(high) || !(original > 0.0) || !std::isfinite(original)))
+        return LORA_ERR_INVALID_ARG;
+    const double two_pi = 6.283185307179586477;
+    if (scaling == LORA_ROPE_NTK && rot > 2)
+        base *= std::pow(factor, (double)rot / (rot - 2));
+    double first = 0, last = 0;      // yarn: the ramp's pairs
+    if (scaling == LORA_ROPE_YARN) {
+        // the pair that makes `turns` turns over the original length
+        const double per = rot / (2.0 * std::log(base));
+        first = std::fmax(std::floor(per * std::log(original / (high * two_pi))), 0.0);
+        last = std::fmin(std::ceil(per * std::log(original / (low * two_pi))), rot - 1.0);
+    }
+    for (int j = 0; j < rot / 2; ++j) {
+        double f = std::pow(base, -2.0 * j / rot);
+        double stretched = 0;        // share of the frequency that is divided by factor
+        if (scaling == LORA_ROPE_LINEAR)
+            stretched = 1;
+        else if (scaling == LORA_ROPE_BANDS)
+            stretched = 1 - (original * f / two_pi - low) / (high - low);
+        else if (scaling == LORA_ROPE_YARN)
+            stretched = (j - first) / std::fmax(last - first, 0.001);
+        stretched = std::fmin(std::fmax(stretched, 0.0), 1.0);
+        freq[j] = f * (1 - stretched) + f / factor * stretched;
+        if (stretched == 0)
+            freq[j] = f;
+    }
+    *mscale = scaling == LORA_ROPE_YARN && factor > 1.0 ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    return LORA_OK;
+}

@@ -80,6 +80,9 @@ extern "C" {
 #define LORA_MAX_ADAPTERS 32768
 #define LORA_MAX_ADS_PER_REQ 8
 #define LORA_MAX_PROJ 4          /* projections sharing one input (lora_sgmv_shrink_proj, _apply_proj) */
+#define LORA_MAX_I8_IN 65536     /* d_in of the 8-bit projections: sums of 8-bit products stay inside 32 bits */
+#define LORA_MAX_ROPE_DIM 1024   /* head dimension of lora_rope */
+#define LORA_MAX_ROPE_HEADS 4096 /* heads of all the tensors of one lora_rope call */
 
 /* Status codes.  Host-side codes are returned directly; device-side codes are
  * bits of the workspace error word returned by lora_get_error (OR-ed). */
@@ -93,6 +96,9 @@ typedef enum {
     LORA_ERR_WORKSPACE = 32,    /* host: workspace null, misaligned or too small */
     LORA_ERR_TIMEOUT = 64       /* device: a pipeline wait inside a kernel expired (work skipped) */
 } lora_status;
+
+/* Element types of the entry points that take more than bf16. */
+typedef enum { LORA_BF16 = 0, LORA_F16 = 1, LORA_F32 = 2 } lora_dtype;
 
 /* One projection's resident adapter pool ("all LoRAs stay resident", same
  * page, section "Placement").  The struct itself is a HOST object read during
@@ -120,7 +126,9 @@ typedef enum {
     LORA_OP_ROUTE = 4,
     LORA_OP_MERGE = 5,
     LORA_OP_LINEAR = 6,
-    LORA_OP_APPLY_PROJ = 7      /* max_rank = the projections' max_rank summed */
+    LORA_OP_APPLY_PROJ = 7,     /* max_rank = the projections' max_rank summed */
+    LORA_OP_LINEAR_I8 = 8,      /* n_adapters, max_rank and n_items are ignored */
+    LORA_OP_LINEAR_I8_SGMV = 9
 } lora_op;
 
 /* Bytes of workspace `op` needs for N token rows.  n_items = n_seg for the
@@ -265,6 +273,109 @@ LORA_API lora_status lora_sgmv_apply_proj(const void *X, int64_t ldx, void *cons
 LORA_API lora_status lora_linear_sgmv(const void *X, int64_t ldx, const void *W, int64_t ldw, void *Y, int64_t ldy,
                              const lora_pool *pool, const int32_t *seg_off, const int32_t *seg_ad,
                              int32_t n_seg, int32_t N, float scale, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * lora_quant_i8 -- rows as 8-bit integers with one scale each, the operands of
+ * lora_linear_i8: the tokens of a call, or once the rows (output channels) of
+ * a base weight.
+ *   S[n] = max_i |X[n][i]| / 127 (fp32),   Q[n][i] = round(127 X[n][i] / max_i |X[n][i]|),
+ * the exact quotient rounded to the nearest integer, halves to even.  A row of
+ * zeros gives S = 0 and Q = 0.  A row with an infinity or a NaN gives S = NaN
+ * and Q = 0, so that its products are NaN.
+ * X: device [N, d] of `dtype` (lora_dtype), leading dimension ldx, d and ldx
+ * multiples of 8, 16-byte aligned.  Q: device int8 [N, d], ldq a multiple of
+ * 16, 16-byte aligned; bytes between d and ldq are not written.  S: device
+ * fp32 [N].  One launch, no workspace.
+ */
+LORA_API lora_status lora_quant_i8(const void *X, int32_t dtype, int64_t ldx, int8_t *Q, int64_t ldq, float *S,
+                             int32_t N, int32_t d, void *stream);
+
+/*
+ * lora_linear_i8 -- a projection whose base weight is held in 8 bits, with one
+ * scale per token and one per output channel:
+ *   Y[n][o] = Sx[n] Sw[o] sum_i Q[n][i] Wq[o][i],
+ * the sum exact in 32-bit integers, the scaled result fp32, rounded to Y's type
+ * once.  Y is OUTPUT ONLY.  Q [N, d_in] and Wq [d_out, d_in]: device int8,
+ * leading dimensions multiples of 16, 16-byte aligned (any values, -128
+ * included); Sx fp32 [N], Sw fp32 [d_out], applied as they are (NaN and
+ * infinities propagate); Y: device [N, d_out] of `dtype` (lora_dtype), ldy as
+ * elsewhere.  d_in and d_out multiples of 8, d_in <= LORA_MAX_I8_IN.  One
+ * launch from one token to long prompts; a decode batch with adapters follows
+ * it with lora_bgmv on the same Y.  Workspace: its header only (the error word,
+ * lora_workspace_size(LORA_OP_LINEAR_I8, N, 1, d_in, d_out, 8, 0, 1)).  Needs
+ * tensor maps (B200): LORA_ERR_UNSUPPORTED where they cannot be built.
+ */
+LORA_API lora_status lora_linear_i8(const int8_t *Q, int64_t ldq, const float *Sx, const int8_t *Wq, int64_t ldw,
+                              const float *Sw, void *Y, int32_t dtype, int64_t ldy, int32_t N, int32_t d_in,
+                              int32_t d_out, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * lora_linear_i8_sgmv -- the adapted projection over an 8-bit base weight: what
+ * lora_linear_sgmv computes with W X[n] replaced by lora_linear_i8's product,
+ *   Y[n][o] = Sx[n] Sw[o] sum_i Q[n][i] Wq[o][i] + scale * sum_{j < rank[a]} B[a][o][j] V[n][j],
+ *   V[n][j] = sum_i A[a][j][i] X[n][i],
+ * for seg_off[k] <= n < seg_off[k+1], a = seg_ad[k]; seg_ad[k] = -1: no delta.
+ * The delta reads the tokens X (bf16) themselves, not their 8-bit form.  Rows
+ * outside every segment are not written.  Y is bf16, OUTPUT ONLY, rounded once.
+ * Q, Sx, Wq, Sw as for lora_linear_i8; X, Y, pool, segments and device errors
+ * as for lora_linear_sgmv.  Workspace: lora_workspace_size(LORA_OP_LINEAR_I8_SGMV,
+ * N, n_adapters, d_in, d_out, max_rank, n_seg, 0).  Three launches.
+ */
+LORA_API lora_status lora_linear_i8_sgmv(const int8_t *Q, int64_t ldq, const float *Sx, const void *X, int64_t ldx,
+                              const int8_t *Wq, int64_t ldw, const float *Sw, void *Y, int64_t ldy,
+                              const lora_pool *pool, const int32_t *seg_off, const int32_t *seg_ad,
+                              int32_t n_seg, int32_t N, float scale, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * lora_rope -- rotary positions on the heads of up to LORA_MAX_PROJ tensors
+ * that share their tokens, in one launch (q and k after their adapted
+ * projection).  With t = pos[n] * freq[j], the pair (a, b) of head dimensions
+ * (j, j + rot/2), or (2j, 2j + 1) if `interleaved`, becomes
+ *   a' = mscale (a cos t - b sin t),   b' = mscale (b cos t + a sin t)
+ * for j < rot/2; dimensions from rot to dim are copied.  `inverse` turns by -t
+ * (times mscale): the gradient of the call with the same arguments.  The angle
+ * is formed and reduced in fp64, the rotation is fp32, each output is rounded
+ * once.
+ * mats: HOST array; x and y are device tensors of `dtype` with element strides
+ * between tokens and between heads and unit stride inside a head.  y may be x
+ * with the same strides (in place); otherwise no element of any y may overlap
+ * any x or any other y.  x strides may be 0 (one token or head read for all);
+ * y's tokens and heads must lie apart.  pos: device int32 or int64 [N]
+ * (pos_bytes 4 or 8), any value, negative ones too (exact up to 2^31 turns of
+ * a pair).  freq: device fp64 [rot/2], radians per position (lora_rope_freqs
+ * fills them).  rot even, 2 <= rot <= dim <= LORA_MAX_ROPE_DIM; any odd sizes
+ * and strides are taken, 16-byte accesses are used where sizes, strides and
+ * addresses allow.  One launch, no workspace.
+ */
+typedef struct lora_rope_mat {
+    const void *x;
+    void *y;
+    int64_t x_token, x_head;   /* element strides of x */
+    int64_t y_token, y_head;   /* element strides of y */
+    int32_t heads;
+} lora_rope_mat;
+LORA_API lora_status lora_rope(const lora_rope_mat *mats, int32_t n_mats, int32_t dtype, const void *pos,
+                               int32_t pos_bytes, const double *freq, int32_t N, int32_t dim, int32_t rot,
+                               int32_t interleaved, int32_t inverse, float mscale, void *stream);
+
+/*
+ * lora_rope_freqs -- the rot/2 frequencies of lora_rope, f_j = base^(-2j/rot), and
+ * the factor on the rotated values, for a context stretched by `factor` in one
+ * of the usual ways (host function, HOST pointers):
+ *   NONE    as they are;
+ *   LINEAR  every f_j / factor;
+ *   NTK     base replaced by base * factor^(rot/(rot-2));
+ *   BANDS   by the turns original * f_j / 2 pi a pair makes over the original
+ *           length: from `high` turns on unchanged, up to `low` turns f_j / factor,
+ *           linear in the turns between;
+ *   YARN    linear in j between the pairs that make `high` and `low` turns (rounded
+ *           outwards, kept in [0, rot-1]), and mscale = 0.1 ln(factor) + 1
+ *           (1 for a factor up to 1; mscale is 1 in every other form).
+ * low, high and original are read by BANDS and YARN only (0 < low < high).
+ */
+enum { LORA_ROPE_NONE = 0, LORA_ROPE_LINEAR = 1, LORA_ROPE_NTK = 2, LORA_ROPE_BANDS = 3, LORA_ROPE_YARN = 4 };
+LORA_API lora_status lora_rope_freqs(int32_t scaling, int32_t rot, double base, double factor, double low,
+                                     double high, double original, double *freq, double *mscale);
 
 /*
  * lora_sgmv_expand -- the second half of the segmented product:

@@ -1,0 +1,405 @@
+"""The 8-bit projection (lora_quant_i8, lora_linear_i8, lora_linear_i8_sgmv) against its
+definition in 64 bits.
+
+Tolerances, each from the roundings on the way and set before the first run:
+* quantised integers: none, they are the exact quotient rounded (ties to even); a scale is
+  one fp32 division, equal to numpy's;
+* lora_linear_i8: the integer sum is exact; its conversion to fp32, the product of the two
+  scales and the scaling are one rounding each (2^-24 relative), the store is half a step
+  of the output type (fp32: the scaling is the store);
+* lora_linear_i8_sgmv: the bars of the bf16 projection (test_gpu_linear.py): the parity
+  bound, and at least 99 % of the outputs the correctly rounded bf16.
+"""
+import numpy as np
+import pytest
+import torch
+
+import adapter_gemv_sgmv_b200 as L
+import oracle
+from helpers import DevPool, check_parity, check_rounded, dev_bf16, rand_host_pool, rand_x, scatter_pool, widen
+from workloads import to_host
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+def _i32(a):
+    return torch.tensor(np.asarray(a, np.int32), device=DEV)
+
+
+def _padded_i8(n, d, pad=0, fill=0):
+    """An int8 [n, d] view whose rows start on 16-byte boundaries, and its whole buffer."""
+    buf = torch.full((n, (d + 15) // 16 * 16 + pad), fill, dtype=torch.int8, device=DEV)
+    return buf[:, :d], buf
+
+
+def _quant_ref(x):
+    """Exact: integers by 80-bit products compared in integers where a half is near."""
+    x = np.asarray(x, np.float64)
+    top = np.abs(x).max(1, keepdims=True)
+    safe = np.where(top > 0, top, 1.0)
+    # 127 x is exact in 64 bits (24 + 7 bits); the quotient is off by 2^-53 of itself, while a
+    # quotient that is no half stays 2^-33 away from one (numerator and top have 31 and 24 bits)
+    q = np.rint(127 * x / safe)
+    s = (top[:, 0].astype(np.float32) / np.float32(127))
+    return q.astype(np.int8), s
+
+
+def _check_quant(x, msg=""):
+    n, d = x.shape
+    Q, _ = _padded_i8(n, d)
+    S = torch.empty(n, dtype=torch.float32, device=DEV)
+    L.lora_quant_i8(x, Q, S)
+    q, s = _quant_ref(x.double().cpu().numpy())
+    got = Q.cpu().numpy()
+    bad = np.argwhere(got != q)
+    assert bad.size == 0, f"{msg}: {len(bad)} integers differ, first at {bad[0]}"
+    assert np.array_equal(S.cpu().numpy(), s), msg
+
+
+# ------------------------------------------------------------------ quantisation
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("n,d", [(1, 8), (3, 24), (37, 1280), (257, 4096), (5, 14336), (2, 32776), (1, 65536),
+                                 (3, 70000)])
+def test_quant_matches_the_definition(t, n, d):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(n * 1000 + d)
+    x = torch.randn(n, d, generator=g, device=DEV).to(t)
+    _check_quant(x, f"{t} {n}x{d}")
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_quant_halves_and_their_neighbours(t):
+    """Rows whose quotients are halves (x = top (k + 1/2) / 127 where that is a value of the
+    type) and the values next to them on both sides."""
+    rows = []
+    for top in (127.0, 254.0, 1.0, 63.5, 2.0 ** -9 * 127, 1.5, 1.9921875):
+        base = torch.tensor([(k + 0.5) * top / 127 for k in range(127)], dtype=torch.float64).to(t)
+        up = torch.nextafter(base.float(), torch.full_like(base.float(), 1e9)).to(t) if t == torch.float32 else \
+            (base.view(torch.int16) + 1).view(t)
+        down = torch.nextafter(base.float(), torch.full_like(base.float(), -1e9)).to(t) if t == torch.float32 else \
+            (base.view(torch.int16) - 1).view(t)
+        row = torch.cat([base, up, down, -base, -up, -down, torch.tensor([top, -top], dtype=t)])
+        row = row[row.double().abs() <= top]
+        row = torch.cat([row, torch.zeros(768 - row.numel(), dtype=t)])
+        rows.append(row)
+    _check_quant(torch.stack(rows).to(DEV), str(t))
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_quant_every_pair_of_mantissas(t):
+    """Every 8-bit mantissa of x against every one of the row's maximum (two binades)."""
+    m = torch.arange(128, 256, dtype=torch.float64)
+    x = torch.cat([m, m / 2, m / 4, -m / 8])
+    rows = [torch.cat([x[x.abs() <= v], torch.zeros(int((x.abs() > v).sum()), dtype=torch.float64), v.view(1),
+                       torch.zeros(7, dtype=torch.float64)]) for v in m]
+    _check_quant(torch.stack(rows).to(t).to(DEV), str(t))
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("e", [-149, -140, -126, -100, -81, -79, 99, 101, 120, 127])
+def test_quant_range_ends(t, e):
+    """Rows near the smallest and the largest magnitudes, subnormal ones among them."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(e + 200)
+    x = (torch.randint(-255, 256, (4, 64), generator=g, device=DEV).double() / 256 * 2.0 ** min(e, 126)).to(t)
+    if e == 127:
+        x = (x.double() * 2).to(t)
+    x[0] = 0
+    n = x.shape[0]
+    Q, _ = _padded_i8(n, 64)
+    S = torch.empty(n, dtype=torch.float32, device=DEV)
+    L.lora_quant_i8(x, Q, S)
+    q, s = _quant_ref(x.double().cpu().numpy())
+    assert np.array_equal(Q.cpu().numpy(), q)
+    assert np.array_equal(S.cpu().numpy(), s)
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_quant_zero_and_non_finite_rows(t):
+    x = torch.ones(6, 136, device=DEV).to(t)
+    x[0] = 0
+    x[1, 77] = float("nan")
+    x[2, 0] = float("inf")
+    x[3, 135] = -float("inf")
+    x[4, 3] = float("nan")
+    x[4, 4] = float("inf")
+    Q, _ = _padded_i8(6, 136)
+    S = torch.zeros(6, device=DEV)
+    L.lora_quant_i8(x, Q, S)
+    assert float(S[0]) == 0 and int(Q[0].abs().max()) == 0
+    assert torch.isnan(S[1:5]).all() and int(Q[1:5].abs().max()) == 0
+    assert torch.all(Q[5] == 127) and float(S[5]) == float(np.float32(1) / np.float32(127))
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_quant_strided_rows_and_untouched_padding(t):
+    buf = torch.randn(19, 400, device=DEV).to(t)
+    x = buf[:, 8:8 + 264]
+    Q, whole = _padded_i8(19, 264, pad=32, fill=99)
+    S = torch.full((21,), -1.0, device=DEV)
+    L.lora_quant_i8(x, Q, S[1:20])
+    q, s = _quant_ref(x.double().cpu().numpy())
+    assert np.array_equal(Q.cpu().numpy(), q)
+    assert np.array_equal(S.cpu().numpy()[1:20], s)
+    assert torch.all(whole[:, 264:] == 99) and float(S[0]) == -1 and float(S[20]) == -1
+
+
+# ---------------------------------------------------------------------- product
+def _half_step(t):
+    return 0.0 if t == torch.float32 else torch.finfo(t).eps / 2
+
+
+def _check_linear(N, d_in, d_out, t, seed=0, Q=None, W=None, ypad=0):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed + N * 7 + d_in * 3 + d_out)
+    q = Q if Q is not None else torch.randint(-127, 128, (N, d_in), generator=g, device=DEV, dtype=torch.int8)
+    w = W if W is not None else torch.randint(-127, 128, (d_out, d_in), generator=g, device=DEV, dtype=torch.int8)
+    Qp, qb = _padded_i8(N, d_in, pad=16, fill=55)       # padding that would show if it were read
+    Wp, wb = _padded_i8(d_out, d_in, pad=16, fill=77)
+    Qp.copy_(q)
+    Wp.copy_(w)
+    Sx = torch.rand(N, generator=g, device=DEV) * 0.01 + 1e-4
+    Sw = torch.rand(d_out, generator=g, device=DEV) * 0.001 + 1e-5
+    Yb = torch.full((N + 2, d_out + ypad), 3.0, dtype=t, device=DEV)
+    Y = Yb[1:N + 1, :d_out]
+    ws = L.lora_linear_i8(Qp, Sx, Wp, Sw, Y)
+    assert L.lora_get_error(ws) == 0
+    acc = q.double() @ w.double().t()
+    want = acc * Sx.double()[:, None] * Sw.double()
+    got = Y.double()
+    tol = want.abs() * (3.001 * 2.0 ** -24 + _half_step(t)) + (2.0 ** -25 if t == torch.float16 else 0)
+    err = (got - want).abs()
+    worst = (err - tol).max()
+    assert float(worst) <= 0, f"N={N} {d_in}->{d_out} {t}: off by {float(err.max())}"
+    # what surrounds the output is left alone
+    assert torch.all(Yb[0] == 3) and torch.all(Yb[N + 1] == 3) and torch.all(Yb[1:N + 1, d_out:] == 3)
+    return Y
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("N", [1, 2, 8, 15, 16, 17, 33, 64, 100, 128, 129, 200, 256, 257, 513, 1100])
+def test_linear_token_counts(N, t):
+    _check_linear(N, 512, 264, t)
+
+
+@pytest.mark.parametrize("d_in", [8, 16, 24, 120, 128, 136, 200, 1280, 4096, 14336])
+@pytest.mark.parametrize("N,d_out", [(1, 8), (5, 72), (37, 1024), (130, 136), (300, 520)])
+def test_linear_shapes(N, d_in, d_out):
+    _check_linear(N, d_in, d_out, torch.bfloat16, ypad=8)
+
+
+@pytest.mark.parametrize("N,d_in,d_out", [(1, 4096, 14336), (3, 4096, 4096), (256, 4096, 4096), (1024, 4096, 1024),
+                                          (2011, 1280, 1280), (4099, 4096, 6144)])
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
+def test_linear_model_shapes(N, d_in, d_out, t):
+    _check_linear(N, d_in, d_out, t, ypad=24)
+
+
+@pytest.mark.parametrize("N", [1, 20, 300])
+def test_linear_largest_sums(N):
+    """-128 everywhere at the longest d_in: a sum of 2^30, exact."""
+    d_in, d_out = 65536, 136
+    q = torch.full((N, d_in), -128, dtype=torch.int8, device=DEV)
+    w = torch.full((d_out, d_in), -128, dtype=torch.int8, device=DEV)
+    w[1::2] = 127
+    _check_linear(N, d_in, d_out, torch.float32, Q=q, W=w)
+
+
+def test_linear_refuses_a_longer_sum():
+    with pytest.raises(L.LoraError) as e:
+        q = torch.zeros(2, 65552, dtype=torch.int8, device=DEV)
+        w = torch.zeros(8, 65552, dtype=torch.int8, device=DEV)
+        L.lora_linear_i8(q, torch.ones(2, device=DEV), w, torch.ones(8, device=DEV),
+                         torch.zeros(2, 8, dtype=torch.bfloat16, device=DEV))
+    assert e.value.code == 2
+
+
+@pytest.mark.parametrize("N", [4, 300])
+def test_linear_scales_propagate(N):
+    """A NaN token scale makes its row NaN, a zero one makes it zero; the other rows are unharmed."""
+    q = torch.ones(N, 256, dtype=torch.int8, device=DEV)
+    w = torch.ones(136, 256, dtype=torch.int8, device=DEV)
+    Sx, Sw = torch.ones(N, device=DEV), torch.full((136,), 0.5, device=DEV)
+    Sx[1], Sx[2] = float("nan"), 0.0
+    Sw[5] = float("inf")
+    Y = torch.zeros(N, 136, device=DEV)
+    L.lora_linear_i8(q, Sx, w, Sw, Y)
+    assert torch.isnan(Y[1]).all()
+    assert torch.isinf(Y[0, 5]) and torch.isnan(Y[2, 5])
+    ok = [i for i in range(136) if i != 5]
+    assert torch.all(Y[2, ok] == 0) and torch.all(Y[0, ok] == 128) and torch.all(Y[3:, ok] == 128)
+
+
+def test_linear_one_row_without_padding():
+    """A single row's stride is no stride: 24 bytes long, it is taken as it is."""
+    q = torch.randint(-127, 128, (1, 24), dtype=torch.int8, device=DEV)
+    Wp, _ = _padded_i8(16, 24)
+    Wp.copy_(torch.randint(-127, 128, (16, 24), dtype=torch.int8, device=DEV))
+    Y = torch.zeros(1, 16, device=DEV)
+    L.lora_linear_i8(q, torch.ones(1, device=DEV), Wp, torch.ones(16, device=DEV), Y)
+    assert torch.equal(Y.double(), q.double() @ Wp.double().t())
+
+
+# ---------------------------------------------------------------------- adapted
+def _adapted_inputs(rng, N, d_in, d_out):
+    X = rand_x(rng, N, d_in)
+    x = dev_bf16(X)
+    Q, _ = _padded_i8(N, d_in)
+    Sx = torch.empty(N, device=DEV)
+    L.lora_quant_i8(x, Q, Sx)
+    W = torch.randn(d_out, d_in, device=DEV, generator=torch.Generator(device=DEV).manual_seed(N)) / np.sqrt(d_in)
+    Wq, _ = _padded_i8(d_out, d_in)
+    Sw = torch.empty(d_out, device=DEV)
+    L.lora_quant_i8(W, Wq, Sw)
+    base = (Q.double() @ Wq.double().t()) * Sx.double()[:, None] * Sw.double()
+    return X, x, Q, Sx, Wq, Sw, base.cpu().numpy()
+
+
+def _run_adapted(rng, hp, lens, ads, d_in, d_out, scale, start=5, tail=11, what=""):
+    seg_off = np.concatenate([[start], start + np.cumsum(lens)]).astype(np.int32)
+    N = int(seg_off[-1]) + tail
+    X, x, Q, Sx, Wq, Sw, base = _adapted_inputs(rng, N, d_in, d_out)
+    Y = torch.ones((N, d_out), dtype=torch.bfloat16, device=DEV)
+    ws = L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, DevPool(hp), _i32(seg_off), _i32(ads), scale)
+    assert L.lora_get_error(ws) == 0
+    got = widen(to_host(Y))
+    zero_w = np.zeros((d_out, d_in), np.uint16)
+    delta = oracle.linear_sgmv(X, zero_w, hp, seg_off, np.array(ads, np.int32), scale)
+    inside = np.r_[seg_off[0]:seg_off[-1]]
+    want = base + delta
+    check_parity(got[inside], want[inside], what)
+    check_rounded(got[inside], want[inside], what)
+    outside = np.r_[0:start, seg_off[-1]:N]
+    assert np.all(got[outside] == 1.0), what
+
+
+@pytest.mark.parametrize("d_in,d_out", [(328, 200), (256, 520), (4096, 264), (72, 8)])
+def test_adapted_ragged(d_in, d_out):
+    rng = np.random.default_rng(d_in * 7 + d_out)
+    hp = rand_host_pool(rng, [16, 32, 128, 64, 16], d_in, d_out)
+    _run_adapted(rng, hp, [130, 1, 255, 0, 128, 37, 300, 64], [2, 0, 4, 1, 3, -1, 1, 2], d_in, d_out, 0.75,
+                 what=f"adapted {d_in}x{d_out}")
+
+
+@pytest.mark.parametrize("scatter", [False, True])
+def test_adapted_any_rank(scatter):
+    rng = np.random.default_rng(3 + scatter)
+    d_in, d_out = 192, 648
+    hp = rand_host_pool(rng, [8, 24, 40, 16, 96, 64, 120, 128], d_in, d_out)
+    if scatter:
+        hp = scatter_pool(hp)
+    _run_adapted(rng, hp, [130, 200, 64, 150, 129, 90, 200, 140], np.arange(8, dtype=np.int32), d_in, d_out, 1.5,
+                 what=f"adapted, any rank, scatter={scatter}")
+
+
+def test_adapted_many_short_segments():
+    """Forty segments of one to three tokens, neighbours with different adapters and none."""
+    rng = np.random.default_rng(8)
+    d_in, d_out = 512, 1032
+    hp = rand_host_pool(rng, [8, 64, 128, 32], d_in, d_out)
+    _run_adapted(rng, hp, rng.integers(1, 4, 40), rng.integers(-1, 4, 40).astype(np.int32), d_in, d_out, 0.5,
+                 what="adapted, short segments")
+
+
+def test_adapted_model_shape():
+    rng = np.random.default_rng(9)
+    d_in, d_out = 4096, 1024
+    hp = rand_host_pool(rng, [64, 16, 128], d_in, d_out)
+    _run_adapted(rng, hp, [700, 129, 411, 256], [0, 1, -1, 2], d_in, d_out, 0.5, what="adapted model shape")
+
+
+def test_adapted_degenerate_segments():
+    """Only empty segments: nothing is written; one row in one segment; scale 0 is the base."""
+    rng = np.random.default_rng(6)
+    d_in, d_out = 64, 256
+    hp = rand_host_pool(rng, [16, 32], d_in, d_out)
+    _run_adapted(rng, hp, [0, 0], [0, 1], d_in, d_out, 1.0, start=0, tail=100, what="empty")
+    _run_adapted(rng, hp, [1], [1], d_in, d_out, 0.5, start=0, tail=0, what="one row")
+    _run_adapted(rng, hp, [300], [1], d_in, d_out, 0.0, start=0, tail=0, what="scale 0")
+
+
+def test_adapted_bad_metadata_is_reported():
+    """A bad adapter id: its segment gets the base product and the error bit; decreasing
+    offsets: the error bit, those rows untouched."""
+    rng = np.random.default_rng(12)
+    d_in, d_out, N = 128, 136, 300
+    hp = rand_host_pool(rng, [16, 32], d_in, d_out)
+    X, x, Q, Sx, Wq, Sw, base = _adapted_inputs(rng, N, d_in, d_out)
+    Y = torch.ones((N, d_out), dtype=torch.bfloat16, device=DEV)
+    ws = L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, DevPool(hp), _i32([0, 150, N]), _i32([7, 0]), 1.0)
+    assert L.lora_get_error(ws) == 4
+    check_parity(widen(to_host(Y))[:150], base[:150], "bad adapter: base product")
+    Y.fill_(1.0)
+    ws = L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, DevPool(hp), _i32([0, 150, 100]), _i32([-1, 0]), 1.0)
+    assert L.lora_get_error(ws) & 8
+    assert torch.all(Y[150:] == 1)
+
+
+# ----------------------------------------------------------- together and in graphs
+def test_decode_batch_with_adapters_follows_with_bgmv():
+    rng = np.random.default_rng(20)
+    N, d_in, d_out = 37, 512, 264
+    hp = rand_host_pool(rng, [16, 8, 64], d_in, d_out)
+    X, x, Q, Sx, Wq, Sw, base = _adapted_inputs(rng, N, d_in, d_out)
+    ids = rng.integers(-1, 3, N).astype(np.int32)
+    Y = torch.empty((N, d_out), dtype=torch.bfloat16, device=DEV)
+    L.lora_linear_i8(Q, Sx, Wq, Sw, Y)
+    y0 = widen(to_host(Y))
+    ws = L.lora_bgmv(x, Y, DevPool(hp), _i32(ids), 0.5)
+    assert L.lora_get_error(ws) == 0
+    want = y0 + oracle.bgmv_delta(X, hp, ids, 0.5)
+    check_parity(widen(to_host(Y)), want, "8-bit base, then bgmv")
+
+
+@pytest.mark.parametrize("N", [3, 300])
+def test_captured_and_replayed_on_new_inputs(N):
+    d_in, d_out = 512, 264
+    x = torch.randn(N, d_in, device=DEV).bfloat16()
+    Wq = torch.randint(-127, 128, (d_out, d_in), dtype=torch.int8, device=DEV)
+    Sw = torch.rand(d_out, device=DEV) * 0.01
+    Q = torch.empty(N, d_in, dtype=torch.int8, device=DEV)
+    Sx = torch.empty(N, device=DEV)
+    Y = torch.empty(N, d_out, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        L.lora_quant_i8(x, Q, Sx)
+        L.lora_linear_i8(Q, Sx, Wq, Sw, Y)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.lora_quant_i8(x, Q, Sx)
+        ws = L.lora_linear_i8(Q, Sx, Wq, Sw, Y)
+    for seed in range(3):
+        x.copy_(torch.randn(N, d_in, device=DEV).bfloat16())
+        graph.replay()
+        torch.cuda.synchronize()
+        q, sx = _quant_ref(x.double().cpu().numpy())
+        want = (torch.tensor(q, device=DEV).double() @ Wq.double().t()) * torch.tensor(sx, device=DEV).double()[:, None] * Sw.double()
+        assert float(((Y.double() - want).abs() - want.abs() * 3.001 * 2.0 ** -24).max()) <= 0
+    assert L.lora_get_error(ws) == 0
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with the library's own workspaces do not disturb each other."""
+    rng = np.random.default_rng(30)
+    d_in, d_out = 1024, 1032
+    hp = rand_host_pool(rng, [64, 128], d_in, d_out)
+    pool = DevPool(hp)
+    jobs = []
+    for k, lens in enumerate(([700, 300], [129, 900])):
+        off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+        X, x, Q, Sx, Wq, Sw, base = _adapted_inputs(rng, int(off[-1]), d_in, d_out)
+        ads = np.array([k, 1 - k], np.int32)
+        want = base + oracle.linear_sgmv(X, np.zeros((d_out, d_in), np.uint16), hp, off, ads, 0.5)
+        Y = torch.empty((int(off[-1]), d_out), dtype=torch.bfloat16, device=DEV)
+        jobs.append((x, Q, Sx, Wq, Sw, Y, _i32(off), _i32(ads), want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, Q, Sx, Wq, Sw, Y, off, ads, want, s in jobs:
+            L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, pool, off, ads, 0.5, stream=s)
+    torch.cuda.synchronize()
+    for job in jobs:
+        check_parity(widen(to_host(job[5])), job[8], "two streams")
