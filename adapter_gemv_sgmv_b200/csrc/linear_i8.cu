@@ -3,106 +3,633 @@
 //
 //     y[n][o] = s_x[n] s_w[o] sum_i q[n][i] w[o][i]  (+ s sum_j B[a][o][j] v[n][j])
 //
-// The sum of integer products is exact in 32 bits (d_in <= 65536: at most 2^30).
+// The sum of integer products is exact in 32 bits (d_in <= 65536: at most 2^30); it is
+// widened to fp32, scaled, joined by the delta's fp32 sum and rounded once.
 //
-// Simple form: 64 x 64 output tiles through shared memory, four products an
-// instruction on the CUDA cores; the delta is read from the shrink's high and low
-// bf16 parts.
+// k_i8_pair, long token runs: a pair of CTAs (cluster of 2, tcgen05 cta_group::2) owns a
+// tile of 256 rows x BN outputs; each CTA holds 128 rows in its tensor memory and loads
+// 128 token rows and half of the tile's weight rows per 128-byte k-block, so a weight
+// byte crosses from L2 once per 256 rows and a token byte once per BN outputs.
+// Persistent, 320 threads a CTA:
+//   warp 0     producer: TMA boxes into a ring; both CTAs' boxes complete on the
+//              leader's barrier;
+//   warp 1     (leader) one thread issues tcgen05.mma kind::i8 (M = 256, K = 32);
+//   warps 2-9  epilogue: tensor memory -> scale -> y.
+// Two integer accumulators alternate, so a tile's epilogue runs under the next one's
+// products.  The delta (LORA) takes a third, fp32 accumulator: bf16 k-blocks of
+// (s v) high and low parts against the adapter's B columns.  The two tiles of a pair may
+// belong to different adapters; each adapter's k-blocks then make a pass of their own,
+// and a CTA takes the pass of its adapter only (a row must never meet another
+// adapter's B, not even with factors of zero: that B may hold an infinity).
 
 #include "lora_internal.cuh"
+#include "tc_ptx.cuh"
 
 #include <cuda_fp16.h>
 
 namespace lora {
 namespace {
 
-constexpr int kST = 64;     // rows and outputs per tile
-constexpr int kSK = 64;     // bytes of the reduction per step
+constexpr int kPThreads = 320;
+constexpr int kPEpiWarps = 8;
+constexpr int kPNsBlock = 8;            // output slices per block of the tile order
+constexpr int kKB = 128;                // bytes of the reduction per k-block
 
-__device__ __forceinline__ void store_as(void *Y, int32_t dtype, int64_t i, float v)
+// -------------------------------------------------------------- pair PTX glue
+__device__ __forceinline__ uint32_t cluster_rank()
 {
-    if (dtype == LORA_BF16)
-        static_cast<__nv_bfloat16 *>(Y)[i] = __float2bfloat16_rn(v);
-    else if (dtype == LORA_F16)
-        static_cast<__half *>(Y)[i] = __float2half_rn(v);
-    else
-        static_cast<float *>(Y)[i] = v;
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
 }
 
-__global__ void __launch_bounds__(256) k_i8_simple(const I8Args p)
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank)
 {
-    __shared__ int a[kST][kSK / 4 + 1], b[kST][kSK / 4 + 1];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    int n0 = blockIdx.y * kST, rows = min(kST, p.N - n0), ad = -1, r = 0;
-    int64_t ao = 0, bo = 0;
-    if (p.groups) {
-        const int tile = blockIdx.y / 2, part = blockIdx.y & 1;
-        if (tile >= p.hdr->n_groups)
-            return;
-        const Group g = p.groups[tile];
-        n0 = g.p0 + part * kST;
-        rows = min(kST, g.cnt - part * kST);
-        ad = p.seg_ad[g.item];
-        if (ad != -1 && !pool_adapter_ok(p.pool, ad, &r, &ao, &bo)) {
-            if (threadIdx.x == 0)
-                atomicOr(p.err, (uint32_t)LORA_ERR_BAD_ADAPTER);
-            r = 0;
-        }
-    }
-    if (rows <= 0)
-        return;
-    const int o0 = blockIdx.x * kST, outs = min(kST, p.d_out - o0);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    int acc[4][4] = {};
-    for (int k0 = 0; k0 < p.d_in; k0 += kSK) {
-        for (int e = threadIdx.x; e < kST * kSK / 4; e += 256) {
-            const int i = e / (kSK / 4), c = e % (kSK / 4), k = k0 + 4 * c;
-            a[i][c] = i < rows && k < p.d_in ? *reinterpret_cast<const int *>(p.Q + (int64_t)(n0 + i) * p.ldq + k) : 0;
-            b[i][c] = i < outs && k < p.d_in ? *reinterpret_cast<const int *>(p.W + (int64_t)(o0 + i) * p.ldw + k) : 0;
-        }
-        __syncthreads();
-        for (int c = 0; c < kSK / 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = __dp4a(a[ty + 16 * i][c], b[tx + 16 * j][c], acc[i][j]);
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int n = ty + 16 * i, o = tx + 16 * j;
-            if (n >= rows || o >= outs)
-                continue;
-            float v = p.Sx[n0 + n] * p.Sw[o0 + o] * (float)acc[i][j];
-            if (r) {
-                const __nv_bfloat16 *vb = p.Vb + (int64_t)(n0 + n) * p.ldvb;
-                const __nv_bfloat16 *B = p.pool.B + bo + (int64_t)(o0 + o) * r;
-                float d = 0.f;
-                for (int k = 0; k < r; ++k)
-                    d += ((float)vb[k] + (float)vb[p.kv + k]) * (float)B[k];
-                v += d;
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    return a;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void remote_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// mbar_wait for a barrier that the other CTA of the pair arrives on too
+__device__ __forceinline__ bool pair_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err,
+                                          unsigned long long limit_ns)
+{
+    bool ok = try_wait_cluster(bar, parity);
+    if (!ok) {
+        const unsigned long long t0 = now_ns();
+        for (uint32_t i = 1; !ok; ++i) {
+            ok = try_wait_cluster(bar, parity);
+            if (!ok && (i & 63) == 0) {
+                if (*abort_flag)
+                    break;
+                if (now_ns() - t0 > limit_ns) {
+                    *abort_flag = 1;
+                    atomicOr(err, (uint32_t)LORA_ERR_TIMEOUT);
+                    break;
+                }
             }
-            store_as(p.Y, p.dtype, (int64_t)(n0 + n) * p.ldy + o0 + o, v);
         }
+    }
+    return __all_sync(0xffffffffu, ok);
 }
 
-}  // namespace
-
-cudaError_t launch_linear_i8(const I8Args &a, int max_tiles, cudaStream_t s)
+// A box into this CTA's shared memory, completing on a barrier of the pair's leader.
+__device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y,
+                                              uint64_t policy)
 {
-    const int rows = a.groups ? 2 * max_tiles : (a.N + kST - 1) / kST;
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4}], [%2], %5;"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(bar), "r"(x), "r"(y), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_i8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// Arrive on the barrier at this offset in both CTAs when the MMAs issued so far complete.
+__device__ __forceinline__ void commit_pair(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(smem_u32(bar)), "h"((uint16_t)3)
+        : "memory");
+}
+
+// Signed 8-bit A and B, 32-bit integer D, both K-major, M x N.
+__host__ __device__ constexpr uint32_t idesc_i8(int M, int N)
+{
+    return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// ------------------------------------------------------------------ the tiles
+template <bool LORA> struct PairCfg;
+template <> struct PairCfg<false> {
+    static constexpr int BN = 256, stages = 6;
+};
+template <> struct PairCfg<true> {
+    static constexpr int BN = 160, stages = 8;       // 2 integer + 1 fp32 accumulator: 480 of 512 columns
+};
+
+struct PairTc {
+    I8Args a;
+    CUtensorMap map_q;       // tokens [N, d_in], boxes 128 bytes x 128 rows, 128-byte swizzle
+    CUtensorMap map_w;       // weight [d_out, d_in], boxes 128 bytes x BN / 2 rows
+    CUtensorMap map_v;       // LORA: s V as bf16 parts [N, 2 kv], boxes 64 columns x 128 rows
+    CUtensorMap map_b[4];    // LORA: B pool as [B_elems / r, r], r = 16 << m, boxes of min(r, 64) x BN / 2 rows
+    int32_t b_tma;
+    unsigned long long wait_ns;
+    int32_t test_stall;
+};
+
+struct PairTile {
+    int pair, ns;
+};
+
+// Tile u in the blocked order: block k holds every row pair against slices 8k .. 8k + 7,
+// row-major inside, so the tiles in flight share a few MB of tokens and weights in L2.
+__device__ __forceinline__ PairTile pair_tile(int64_t u, int n_pairs, int n_ns)
+{
+    const int64_t per_blk = (int64_t)n_pairs * kPNsBlock;
+    const int blk = (int)(u / per_blk);
+    const int64_t rem = u - blk * per_blk;
+    const int nsb = min(kPNsBlock, n_ns - blk * kPNsBlock);
+    PairTile t;
+    t.pair = (int)(rem / nsb);
+    t.ns = blk * kPNsBlock + (int)(rem - (int64_t)t.pair * nsb);
+    return t;
+}
+
+struct PairAd {
+    int32_t a;      // adapter, -1: none
+    int r;          // rank, 0: no delta
+    int m;          // B view, -1: rows gathered
+    int brow;       // row of output 0 in that view
+    int64_t boff;
+};
+
+__device__ PairAd pair_adapter(const PairTc &p, int item, bool report)
+{
+    PairAd d = {-1, 0, -1, 0, 0};
+    const int32_t a = p.a.seg_ad[item];
+    int32_t r = 0;
+    int64_t ao = 0, bo = 0;
+    if (a == -1)
+        return d;
+    if (!pool_adapter_ok(p.a.pool, a, &r, &ao, &bo)) {
+        if (report)
+            atomicOr(p.a.err, (uint32_t)LORA_ERR_BAD_ADAPTER);
+        return d;
+    }
+    d.a = a;
+    d.r = r;
+    d.boff = bo;
+    const int m = b_map(r);
+    // (the view's row index of the last box has to fit 32 bits)
+    if (m >= 0 && ((p.b_tma >> m) & 1) && bo % r == 0 && bo / r + p.a.d_out + 512 <= 0x7fffffffLL) {
+        d.m = m;
+        d.brow = (int)(bo / r);
+    }
+    return d;
+}
+
+// The row tiles of a pair and the delta's passes: pass 0 takes the first tile's adapter
+// (and the second's, if it is the same), pass 1 the second's.
+struct PairRows {
+    int row[2], cnt[2];
+    PairAd ad[2];
+    bool same;
+    int nf[2];           // bf16 k-blocks of each pass
+};
+
+__device__ __forceinline__ int delta_kblocks(int r) { return 2 * ((r + 63) >> 6); }
+
+template <bool LORA>
+__device__ __forceinline__ PairRows pair_rows(const PairTc &p, int pair, int n_tiles, bool report)
+{
+    PairRows x;
+    if constexpr (LORA) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const bool has = 2 * pair + t < n_tiles;
+            const Group g = p.a.groups[has ? 2 * pair + t : 2 * pair];
+            x.row[t] = has ? g.p0 : p.a.N;           // past the end: boxes of zeros
+            x.cnt[t] = has ? g.cnt : 0;
+            x.ad[t] = has ? pair_adapter(p, g.item, report) : PairAd{-1, 0, -1, 0, 0};
+        }
+        x.same = x.ad[0].r && x.ad[0].a == x.ad[1].a;
+        x.nf[0] = x.ad[0].r ? delta_kblocks(x.ad[0].r) : 0;
+        x.nf[1] = x.ad[1].r && !x.same ? delta_kblocks(x.ad[1].r) : 0;
+    } else {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            x.row[t] = pair * 256 + t * 128;
+            x.cnt[t] = max(0, min(128, p.a.N - x.row[t]));
+        }
+        x.same = false;
+        x.nf[0] = x.nf[1] = 0;
+    }
+    return x;
+}
+
+__device__ __forceinline__ void tmem_ld16_raw(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// (a compiler-visible dependence keeps the registers' first use behind the wait)
+template <int N> __device__ __forceinline__ void tmem_wait(uint32_t (&r)[N])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("" : "+r"(r[i]));
+}
+
+// 8 scaled results to y
+__device__ __forceinline__ void store8(void *Y, int32_t dtype, int64_t at, const float (&v)[8])
+{
+    if (dtype == LORA_F32) {
+        float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(Y) + at);
+        d[0] = make_float4(v[0], v[1], v[2], v[3]);
+        d[1] = make_float4(v[4], v[5], v[6], v[7]);
+        return;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (dtype == LORA_BF16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    }
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(Y) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool LORA>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_pair(const __grid_constant__ PairTc p)
+{
+    using C = PairCfg<LORA>;
+    constexpr int BN = C::BN, kStages = C::stages;
+    constexpr int kStage = kAtom + BN / 2 * 128;     // token box, half of the weight box
+    constexpr int kF = 2 * BN;                       // LORA: first column of the fp32 accumulator
+    constexpr int kCols = BN / 2;                    // columns an epilogue warp takes
+    extern __shared__ __align__(1024) unsigned char sm_dyn[];
+    // (the two CTAs' buffers must lie at the same offset: the launch gives both the same base)
+    unsigned char *sm = sm_dyn + ((1024 - (smem_u32(sm_dyn) & 1023)) & 1023);
+    __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
+    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], f_full, f_empty, mma_drain;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const int G = gridDim.x / 2, c0 = blockIdx.x / 2;
+    const int n_kb = (p.a.d_in + kKB - 1) / kKB;
+    const int n_ns = (p.a.d_out + BN - 1) / BN;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full_bar[s], LORA ? 2 : 1);   // leader's expect_tx; LORA: and the other CTA's boxes are out
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 2 * kPEpiWarps);
+        }
+        mbar_init(&f_full, 1);
+        mbar_init(&f_empty, 2 * kPEpiWarps);
+        mbar_init(&mma_drain, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    pdl_wait();
+    pdl_trigger();
+    const int n_tiles = LORA ? p.a.hdr->n_groups : 0;
+    const int n_pairs = LORA ? (n_tiles + 1) / 2 : (p.a.N + 255) / 256;
+    const int64_t n_units = (int64_t)n_pairs * n_ns;
+    int issued = 0;
+
+    if (warp == 0) {
+        // ------------------------------------------------ producer (both CTAs)
+        int it = 0;
+        if (p.test_stall)
+            goto done;
+        const uint64_t pol_x = policy_evict_first(), pol_w = policy_evict_last();
+        for (int64_t u = c0; u < n_units; u += G) {
+            const PairTile un = pair_tile(u, n_pairs, n_ns);
+            const PairRows pr = pair_rows<LORA>(p, un.pair, n_tiles, lane == 0 && un.ns == 0 && rank == 0);
+            const int n_all = pr.nf[0] + n_kb + pr.nf[1];
+            const int o0 = un.ns * BN + (int)rank * (BN / 2);
+            const int row = pr.row[rank];
+            for (int k = 0; k < n_all; ++k, ++it) {
+                const int s = it % kStages;
+                if (!warp_wait(&empty_bar[s], ((it / kStages) & 1) ^ 1, &abort_flag, p.a.err, p.wait_ns))
+                    goto done;
+                unsigned char *as = sm + s * kStage, *bs = as + kAtom;
+                const int kb = k - pr.nf[0];
+                const uint32_t bar = map_rank(smem_u32(&full_bar[s]), 0);
+                if (!LORA || (kb >= 0 && kb < n_kb)) {
+                    if (lane == 0) {
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(&full_bar[s], 2 * kStage);
+                        else if (LORA)
+                            remote_arrive(bar);
+                        tma_load_pair(as, &p.map_q, bar, kb * kKB, row, pol_x);
+                        tma_load_pair(bs, &p.map_w, bar, kb * kKB, o0, pol_w);
+                    }
+                } else {
+                    // delta k-block j of a pass: part j % 2 (high, low) of rank columns 64 (j / 2) ..
+                    const int pass = kb < 0 ? 0 : 1;
+                    const int j = pass ? kb - n_kb : k;
+                    const PairAd ad = pass ? pr.ad[1] : pr.ad[0];
+                    const int c = j >> 1, w = ad.r < 64 ? ad.r : 64;
+                    const bool mine = pr.same || pass == (int)rank;
+                    if (ad.m < 0) {
+                        // no view of this rank: all lanes gather the CTA's BN / 2 output rows x 64
+                        // rank columns (128-byte swizzle); past r and past d_out zeros
+                        for (int idx = lane; idx < BN / 2 * 8; idx += 32) {
+                            const int o = idx >> 3, cc = idx & 7, col = c * 64 + cc * 8;
+                            const bool ok = o0 + o < p.a.d_out && col < ad.r;
+                            const __nv_bfloat16 *src =
+                                ok ? p.a.pool.B + ad.boff + (int64_t)(o0 + o) * ad.r + col : p.a.pool.B;
+                            cp_async16(smem_u32(bs) + sw128_off(o, cc), src, ok);
+                        }
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        fence_async_smem();
+                        __syncwarp();
+                    }
+                    if (lane == 0) {
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(&full_bar[s],
+                                                  (uint32_t)(2 * (kAtom + (ad.m >= 0 ? BN / 2 * w * 2 : 0))));
+                        else
+                            remote_arrive(bar);
+                        // (the other adapter's rows are never read, but a box has to arrive)
+                        tma_load_pair(as, &p.map_v, bar, (j & 1) * p.a.kv + c * 64, mine ? row : p.a.N, pol_x);
+                        if (ad.m >= 0)
+                            tma_load_pair(bs, &p.map_b[ad.m], bar, c * 64, ad.brow + o0, pol_w);
+                    }
+                }
+                __syncwarp();
+                issued = it + 1;
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (leader)
+        int it = 0, t = 0, fp = 0;
+        const uint32_t idesc = idesc_i8(256, BN), idesc_f = idesc_bf16(256, BN);
+        for (int64_t u = c0; u < n_units && rank == 0; u += G, ++t) {
+            const PairTile un = pair_tile(u, n_pairs, n_ns);
+            const PairRows pr = pair_rows<LORA>(p, un.pair, n_tiles, false);
+            const int n_all = pr.nf[0] + n_kb + pr.nf[1];
+            const int b = t & 1;
+            for (int k = 0; k < n_all; ++k, ++it) {
+                const int s = it % kStages;
+                const int kb = k - pr.nf[0];
+                const bool base = !LORA || (kb >= 0 && kb < n_kb);
+                if (base && kb == 0 &&
+                    !pair_wait(&acc_empty[b], ((t >> 1) & 1) ^ 1, &abort_flag, p.a.err, p.wait_ns))
+                    goto done;
+                if (LORA && (k == 0 || kb == n_kb) && !base) {
+                    if (!pair_wait(&f_empty, (fp & 1) ^ 1, &abort_flag, p.a.err, p.wait_ns))
+                        goto done;
+                    ++fp;
+                }
+                if (!pair_wait(&full_bar[s], (it / kStages) & 1, &abort_flag, p.a.err, p.wait_ns))
+                    goto done;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t as = smem_u32(sm + s * kStage), bs = as + kAtom;
+                    if (base) {
+#pragma unroll
+                        for (int i = 0; i < kKB / 32; ++i)
+                            mma_i8_pair(tmem + b * BN, sw128_desc(as + i * 32), sw128_desc(bs + i * 32), idesc,
+                                        (kb > 0 || i > 0) ? 1u : 0u);
+                    } else {
+                        const int pass = kb < 0 ? 0 : 1;
+                        const int j = pass ? kb - n_kb : k;
+                        const PairAd ad = pass ? pr.ad[1] : pr.ad[0];
+                        const int left = ad.r - (j >> 1) * 64;
+                        const int steps = ((left < 64 ? left : 64) + 15) >> 4;
+                        for (int i = 0; i < steps; ++i) {
+                            // B columns in their view's swizzle
+                            const uint64_t bd = ad.r >= 64 || ad.m < 0 ? sw128_desc(bs + i * 32)
+                                              : (ad.r == 32 ? sw64_desc(bs + i * 32) : sw32_desc(bs));
+                            mma_bf16_pair(tmem + kF, sw128_desc(as + i * 32), bd, idesc_f,
+                                          (j > 0 || i > 0) ? 1u : 0u);
+                        }
+                    }
+                    commit_pair(&empty_bar[s]);
+                    if (base && kb == n_kb - 1)
+                        commit_pair(&acc_full[b]);
+                    if (LORA && !base && (kb == -1 || k == n_all - 1))
+                        commit_pair(&f_full);
+                }
+                __syncwarp();
+            }
+        }
+    } else {
+        // ------------------------------------------------ epilogue (both CTAs)
+        const int q = warp & 3;                      // TMEM lane quarter
+        const int half = (warp - 2) >> 2;            // columns [half * kCols, + kCols)
+        const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + half * kCols;
+        int t = 0, fp = 0;
+        for (int64_t u = c0; u < n_units; u += G, ++t) {
+            const PairTile un = pair_tile(u, n_pairs, n_ns);
+            const PairRows pr = pair_rows<LORA>(p, un.pair, n_tiles, false);
+            const int b = t & 1, r = q * 32 + lane;
+            const int row = pr.row[rank] + r;
+            const bool valid = r < pr.cnt[rank];
+            const float sx = valid ? __ldg(p.a.Sx + row) : 0.f;
+            const int o0 = un.ns * BN + half * kCols;
+            float f[LORA ? kCols : 1];
+            bool has_f = false;
+            if constexpr (LORA) {
+#pragma unroll 1
+                for (int pass = 0; pass < 2; ++pass) {
+                    if (pr.nf[pass] == 0)
+                        continue;
+                    if (!warp_wait(&f_full, fp & 1, &abort_flag, p.a.err, p.wait_ns))
+                        goto done;
+                    ++fp;
+                    tc_fence_after();
+                    if (pr.same || pass == (int)rank) {
+                        has_f = true;
+#pragma unroll
+                        for (int c = 0; c < kCols; c += 16) {
+                            uint32_t w[16];
+                            tmem_ld16_raw(lane_base + kF + c, w);
+                            tmem_wait(w);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                f[c + i] = __uint_as_float(w[i]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        remote_arrive(map_rank(smem_u32(&f_empty), 0));
+                }
+            }
+            if (!warp_wait(&acc_full[b], (t >> 1) & 1, &abort_flag, p.a.err, p.wait_ns))
+                goto done;
+            tc_fence_after();
+            const int64_t yrow = (int64_t)row * p.a.ldy;
+#pragma unroll
+            for (int c = 0; c < kCols; c += 16) {
+                uint32_t w[16];
+                tmem_ld16_raw(lane_base + b * BN + c, w);
+                tmem_wait(w);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const int o = o0 + c + 8 * g;
+                    if (valid && o < p.a.d_out) {
+                        const float *sw = p.a.Sw + o;
+                        float v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            v[i] = (float)(int)w[8 * g + i] * (sx * __ldg(sw + i));
+                            if (LORA && has_f)
+                                v[i] += f[LORA ? c + 8 * g + i : 0];
+                        }
+                        store8(p.a.Y, p.a.dtype, yrow + o, v);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                remote_arrive(map_rank(smem_u32(&acc_empty[b]), 0));
+        }
+    }
+done:
+    __syncwarp();
+    // nothing may land in shared memory or TMEM, or be read by the pair's MMAs, after
+    // either CTA lets go of them
+    if (warp == 0 && rank == 0)
+        drain_fills(full_bar, kStages, issued, p.a.err, p.wait_ns);
+    if (warp == 1 && rank == 0 && lane == 0) {
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                         smem_u32(&mma_drain))
+                     : "memory");
+        const unsigned long long t0 = now_ns();
+        while (!mbar_try_wait(&mma_drain, 0)) {
+            if (now_ns() - t0 > p.wait_ns) {
+                atomicOr(p.a.err, (uint32_t)LORA_ERR_TIMEOUT);
+                break;
+            }
+        }
+    }
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+// Row-major 8-bit matrix [rows, cols] with leading dimension ld: boxes of 128 bytes x
+// box_rows rows, 128-byte swizzle, zeros outside the matrix.
+bool encode_box8(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld, int box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool LORA> cudaError_t launch_pair(const I8Args &a, int64_t max_tiles, cudaStream_t s, bool *ok)
+{
+    using C = PairCfg<LORA>;
+    PairTc p = {};
+    p.a = a;
+    *ok = encode_box8(&p.map_q, a.Q, a.N, a.d_in, a.ldq, 128) && encode_box8(&p.map_w, a.W, a.d_out, a.d_in, a.ldw, C::BN / 2);
+    if (*ok && LORA) {
+        *ok = encode_box(&p.map_v, a.Vb, a.N, 2 * (int64_t)a.kv, a.ldvb, 128);
+        p.b_tma = encode_b_views(p.map_b, a.pool.B, a.pool.B_elems, C::BN / 2);
+    }
+    if (!*ok)
+        return cudaSuccess;
+    p.wait_ns = wait_bound_ns();
+    p.test_stall = test_stall_mode();
+    const int smem = C::stages * (kAtom + C::BN / 2 * 128) + 1024;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        if ((e = cudaFuncSetAttribute(k_i8_pair<LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+            return e;
+        if (dev >= 0 && dev < 64)
+            attr_set[dev] = true;
+    }
+    const int64_t pairs = LORA ? (max_tiles + 1) / 2 : ((int64_t)a.N + 255) / 256;
+    const int64_t units = pairs * ((a.d_out + C::BN - 1) / C::BN);
+    int clusters = sm_count() / 2;
+    if (units < clusters)
+        clusters = (int)units;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.d_out + kST - 1) / kST, rows);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(2 * clusters);
+    cfg.blockDim = dim3(kPThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_i8_simple, a);
+    return cudaLaunchKernelEx(&cfg, k_i8_pair<LORA>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_i8(const I8Args &a, int max_tiles, cudaStream_t s, bool *ok)
+{
+    return a.groups ? launch_pair<true>(a, max_tiles, s, ok) : launch_pair<false>(a, 0, s, ok);
 }
 
 }  // namespace lora

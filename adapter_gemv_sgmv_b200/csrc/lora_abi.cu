@@ -798,8 +798,9 @@ lora_status lora_linear_i8(const int8_t *Q, int64_t ldq, const float *Sx, const 
     a.d_in = d_in;
     a.d_out = d_out;
     a.err = &static_cast<WsHeader *>(ws)->err;
-    LORA_CUDA(launch_linear_i8(a, 0, (cudaStream_t)stream));
-    return LORA_OK;
+    bool ok = false;
+    LORA_CUDA(launch_linear_i8(a, 0, (cudaStream_t)stream, &ok));
+    return ok ? LORA_OK : LORA_ERR_UNSUPPORTED;
 }
 
 lora_status lora_linear_i8_sgmv(const int8_t *Q, int64_t ldq, const float *Sx, const void *X, int64_t ldx,
@@ -876,8 +877,9 @@ lora_status lora_linear_i8_sgmv(const int8_t *Q, int64_t ldq, const float *Sx, c
     a.Vb = ta.Vb;
     a.ldvb = ta.ldvb;
     a.kv = L.kv;
-    LORA_CUDA(launch_linear_i8(a, max_tiles, s));
-    return LORA_OK;
+    bool ok = false;
+    LORA_CUDA(launch_linear_i8(a, max_tiles, s, &ok));
+    return ok ? LORA_OK : LORA_ERR_UNSUPPORTED;
 }
 
 lora_status lora_sgmv_expand(const float *V, int64_t ldv, void *Y, int64_t ldy,

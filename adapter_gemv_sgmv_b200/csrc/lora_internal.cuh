@@ -335,7 +335,8 @@ struct I8Args {
     int32_t kv;
 };
 
-cudaError_t launch_linear_i8(const I8Args &a, int max_tiles, cudaStream_t s);
+// *ok: the tensor maps could be encoded (else nothing was launched)
+cudaError_t launch_linear_i8(const I8Args &a, int max_tiles, cudaStream_t s, bool *ok);
 
 // Workspace bytes of lora_merge (0 for unsupported sizes).
 size_t merge_workspace_size(int32_t d_in, int32_t d_out, int32_t max_rank);

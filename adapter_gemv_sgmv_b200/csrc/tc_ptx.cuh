@@ -311,9 +311,9 @@ bool encode_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, i
 }
 
 // The B pool seen as [B_elems / r, r] for r = 16, 32, 64, 128 (maps[m], r = 16 << m):
-// boxes of 128 rows (outputs) x min(r, 64) columns, swizzled to the row width.
+// boxes of box_rows rows (outputs) x min(r, 64) columns, swizzled to the row width.
 // Returns the bit mask of the views that could be encoded.
-int encode_b_views(CUtensorMap *maps, const void *B, int64_t B_elems)
+int encode_b_views(CUtensorMap *maps, const void *B, int64_t B_elems, int box_rows = 128)
 {
     int mask = 0;
     EncodeTiledFn fn = encode_fn();
@@ -326,7 +326,7 @@ int encode_b_views(CUtensorMap *maps, const void *B, int64_t B_elems)
             continue;
         const cuuint64_t dims[2] = {(cuuint64_t)r, (cuuint64_t)rows};
         const cuuint64_t strides[1] = {(cuuint64_t)r * 2};
-        const cuuint32_t box[2] = {(cuuint32_t)(r < 64 ? r : 64), 128};
+        const cuuint32_t box[2] = {(cuuint32_t)(r < 64 ? r : 64), (cuuint32_t)box_rows};
         const cuuint32_t estr[2] = {1, 1};
         const CUtensorMapSwizzle sw = r == 16 ? CU_TENSOR_MAP_SWIZZLE_32B
                                     : (r == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
