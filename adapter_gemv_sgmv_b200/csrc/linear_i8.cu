@@ -15,12 +15,17 @@
 //              leader's barrier;
 //   warp 1     (leader) one thread issues tcgen05.mma kind::i8 (M = 256, K = 32);
 //   warps 2-9  epilogue: tensor memory -> scale -> y.
-// Two integer accumulators alternate, so a tile's epilogue runs under the next one's
-// products.  The delta (LORA) takes a third, fp32 accumulator: bf16 k-blocks of
-// (s v) high and low parts against the adapter's B columns.  The two tiles of a pair may
-// belong to different adapters; each adapter's k-blocks then make a pass of their own,
-// and a CTA takes the pass of its adapter only (a row must never meet another
-// adapter's B, not even with factors of zero: that B may hold an infinity).
+// Without adapters two integer accumulators alternate, so a tile's epilogue runs under
+// the next one's products.  The delta (LORA) takes the second half of tensor memory as an
+// fp32 accumulator: bf16 k-blocks of (s v) high and low parts against the adapter's B
+// columns.  The epilogue then empties both into packed registers and lets the next tile
+// start before it stores.  (160 columns, which leave room for two integer accumulators
+// beside the fp32 one, were slower: the kernel is bound by what the SMs read from L2,
+// 10 TB/s, and a tile of 256 x BN reads (256 + BN) / (256 BN) bytes a product.)
+// The two row tiles of a pair may belong to different adapters; the second's delta then
+// makes a pass of its own after the first CTA has emptied its accumulators: a row must
+// never meet another adapter's B, not even with factors of zero, as that B may hold an
+// infinity.
 
 #include "lora_internal.cuh"
 #include "tc_ptx.cuh"
@@ -55,44 +60,11 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// (orders tensor memory accesses only, through the tcgen05 fences around it: a release
+// at cluster scope would wait for the epilogue's stores)
 __device__ __forceinline__ void remote_arrive(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// mbar_wait for a barrier that the other CTA of the pair arrives on too
-__device__ __forceinline__ bool pair_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *err,
-                                          unsigned long long limit_ns)
-{
-    bool ok = try_wait_cluster(bar, parity);
-    if (!ok) {
-        const unsigned long long t0 = now_ns();
-        for (uint32_t i = 1; !ok; ++i) {
-            ok = try_wait_cluster(bar, parity);
-            if (!ok && (i & 63) == 0) {
-                if (*abort_flag)
-                    break;
-                if (now_ns() - t0 > limit_ns) {
-                    *abort_flag = 1;
-                    atomicOr(err, (uint32_t)LORA_ERR_TIMEOUT);
-                    break;
-                }
-            }
-        }
-    }
-    return __all_sync(0xffffffffu, ok);
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // A box into this CTA's shared memory, completing on a barrier of the pair's leader.
@@ -142,10 +114,10 @@ __host__ __device__ constexpr uint32_t idesc_i8(int M, int N)
 // ------------------------------------------------------------------ the tiles
 template <bool LORA> struct PairCfg;
 template <> struct PairCfg<false> {
-    static constexpr int BN = 256, stages = 6;
+    static constexpr int BN = 256, stages = 6, buffers = 2;
 };
 template <> struct PairCfg<true> {
-    static constexpr int BN = 160, stages = 8;       // 2 integer + 1 fp32 accumulator: 480 of 512 columns
+    static constexpr int BN = 256, stages = 6, buffers = 1;
 };
 
 struct PairTc {
@@ -178,73 +150,85 @@ __device__ __forceinline__ PairTile pair_tile(int64_t u, int n_pairs, int n_ns)
 }
 
 struct PairAd {
-    int32_t a;      // adapter, -1: none
     int r;          // rank, 0: no delta
     int m;          // B view, -1: rows gathered
-    int brow;       // row of output 0 in that view
     int64_t boff;
 };
 
-__device__ PairAd pair_adapter(const PairTc &p, int item, bool report)
-{
-    PairAd d = {-1, 0, -1, 0, 0};
-    const int32_t a = p.a.seg_ad[item];
-    int32_t r = 0;
-    int64_t ao = 0, bo = 0;
-    if (a == -1)
-        return d;
-    if (!pool_adapter_ok(p.a.pool, a, &r, &ao, &bo)) {
-        if (report)
-            atomicOr(p.a.err, (uint32_t)LORA_ERR_BAD_ADAPTER);
-        return d;
-    }
-    d.a = a;
-    d.r = r;
-    d.boff = bo;
-    const int m = b_map(r);
-    // (the view's row index of the last box has to fit 32 bits)
-    if (m >= 0 && ((p.b_tma >> m) & 1) && bo % r == 0 && bo / r + p.a.d_out + 512 <= 0x7fffffffLL) {
-        d.m = m;
-        d.brow = (int)(bo / r);
-    }
-    return d;
-}
-
 // The row tiles of a pair and the delta's passes: pass 0 takes the first tile's adapter
-// (and the second's, if it is the same), pass 1 the second's.
-struct PairRows {
-    int row[2], cnt[2];
-    PairAd ad[2];
-    bool same;
-    int nf[2];           // bf16 k-blocks of each pass
+// (and the second's, if it is the same), pass 1 the second's.  Packed, as it lies in
+// shared memory: finding it takes five dependent loads from global memory (tile, segment,
+// adapter, its metadata), more than a microsecond that every role of every tile would
+// wait for, so the CTA's threads look up all of its tiles at once when it starts.
+struct __align__(16) PairRows {
+    int64_t boff[2];
+    int32_t row[2];
+    uint16_t cnt[2];
+    uint16_t ad[2];      // rank | (view index + 1) << 8 | same adapter as tile 0 << 15
+
+    __device__ PairAd adapter(int t) const
+    {
+        PairAd d;
+        d.r = ad[t] & 0xff;
+        d.m = ((ad[t] >> 8) & 7) - 1;
+        d.boff = boff[t];
+        return d;
+    }
+    __device__ bool same() const { return ad[1] >> 15; }
+    // bf16 k-blocks of a pass: high and low parts of every 64 rank columns
+    __device__ int nf(int pass) const { return pass && same() ? 0 : 2 * (((ad[pass] & 0xff) + 63) >> 6); }
 };
+constexpr int kPTable = 256;            // tiles of a CTA looked up when it starts
 
-__device__ __forceinline__ int delta_kblocks(int r) { return 2 * ((r + 63) >> 6); }
-
-template <bool LORA>
-__device__ __forceinline__ PairRows pair_rows(const PairTc &p, int pair, int n_tiles, bool report)
+__device__ PairRows pair_lookup(const PairTc &p, int pair, int n_tiles, bool report)
 {
     PairRows x;
+    int32_t a[2] = {-1, -1};
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        x.row[t] = p.a.N;                            // no tile: boxes past the end, zeros
+        x.cnt[t] = 0;
+        x.ad[t] = 0;
+        x.boff[t] = 0;
+        if (2 * pair + t >= n_tiles)
+            continue;
+        const Group g = p.a.groups[2 * pair + t];
+        x.row[t] = g.p0;
+        x.cnt[t] = (uint16_t)g.cnt;
+        a[t] = p.a.seg_ad[g.item];
+        int32_t r = 0;
+        int64_t ao = 0, bo = 0;
+        if (a[t] == -1)
+            continue;
+        if (!pool_adapter_ok(p.a.pool, a[t], &r, &ao, &bo)) {
+            if (report)
+                atomicOr(p.a.err, (uint32_t)LORA_ERR_BAD_ADAPTER);
+            a[t] = -1;
+            continue;
+        }
+        // (the view's row index of the last box has to fit 32 bits)
+        int m = b_map(r);
+        if (m >= 0 && (!((p.b_tma >> m) & 1) || bo % r != 0 || bo / r + p.a.d_out + 512 > 0x7fffffffLL))
+            m = -1;
+        x.boff[t] = bo;
+        x.ad[t] = (uint16_t)(r | (m + 1) << 8 | (t && a[0] == a[1] ? 0x8000 : 0));
+    }
+    return x;
+}
+
+template <bool LORA>
+__device__ __forceinline__ PairRows pair_rows(const PairTc &p, const PairRows *tab, int i, int pair, int n_tiles)
+{
     if constexpr (LORA) {
+        if (i < kPTable)
+            return tab[i];
+        return pair_lookup(p, pair, n_tiles, false);
+    }
+    PairRows x = {};
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const bool has = 2 * pair + t < n_tiles;
-            const Group g = p.a.groups[has ? 2 * pair + t : 2 * pair];
-            x.row[t] = has ? g.p0 : p.a.N;           // past the end: boxes of zeros
-            x.cnt[t] = has ? g.cnt : 0;
-            x.ad[t] = has ? pair_adapter(p, g.item, report) : PairAd{-1, 0, -1, 0, 0};
-        }
-        x.same = x.ad[0].r && x.ad[0].a == x.ad[1].a;
-        x.nf[0] = x.ad[0].r ? delta_kblocks(x.ad[0].r) : 0;
-        x.nf[1] = x.ad[1].r && !x.same ? delta_kblocks(x.ad[1].r) : 0;
-    } else {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            x.row[t] = pair * 256 + t * 128;
-            x.cnt[t] = max(0, min(128, p.a.N - x.row[t]));
-        }
-        x.same = false;
-        x.nf[0] = x.nf[1] = 0;
+    for (int t = 0; t < 2; ++t) {
+        x.row[t] = pair * 256 + t * 128;
+        x.cnt[t] = (uint16_t)max(0, min(128, p.a.N - x.row[t]));
     }
     return x;
 }
@@ -257,6 +241,14 @@ __device__ __forceinline__ void tmem_ld16_raw(uint32_t taddr, uint32_t (&r)[16])
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
+}
+
+// N consecutive columns (a multiple of 16) of this thread's lane, not yet waited for
+template <int N> __device__ __forceinline__ void tmem_ld16s(uint32_t taddr, uint32_t (&r)[N])
+{
+#pragma unroll
+    for (int c = 0; c < N; c += 16)
+        tmem_ld16_raw(taddr + c, *reinterpret_cast<uint32_t(*)[16]>(&r[c]));
 }
 
 // (a compiler-visible dependence keeps the registers' first use behind the wait)
@@ -297,13 +289,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
     using C = PairCfg<LORA>;
     constexpr int BN = C::BN, kStages = C::stages;
     constexpr int kStage = kAtom + BN / 2 * 128;     // token box, half of the weight box
-    constexpr int kF = 2 * BN;                       // LORA: first column of the fp32 accumulator
+    constexpr int kF = BN;                           // LORA: first column of the fp32 accumulator
+    constexpr int NB = C::buffers;                   // integer accumulators
     constexpr int kCols = BN / 2;                    // columns an epilogue warp takes
     extern __shared__ __align__(1024) unsigned char sm_dyn[];
     // (the two CTAs' buffers must lie at the same offset: the launch gives both the same base)
     unsigned char *sm = sm_dyn + ((1024 - (smem_u32(sm_dyn) & 1023)) & 1023);
     __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
-    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], f_full, f_empty, mma_drain;
+    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], mma_drain;
+    __shared__ PairRows tab[LORA ? kPTable : 1];
+    __shared__ __align__(16) float sw_tile[kPEpiWarps][kCols];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
 
@@ -315,15 +310,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full_bar[s], LORA ? 2 : 1);   // leader's expect_tx; LORA: and the other CTA's boxes are out
+            mbar_init(&full_bar[s], 1);              // leader's expect_tx, for both CTAs' boxes
             mbar_init(&empty_bar[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 2 * kPEpiWarps);
         }
-        mbar_init(&f_full, 1);
-        mbar_init(&f_empty, 2 * kPEpiWarps);
         mbar_init(&mma_drain, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -345,32 +338,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
     const int n_pairs = LORA ? (n_tiles + 1) / 2 : (p.a.N + 255) / 256;
     const int64_t n_units = (int64_t)n_pairs * n_ns;
     int issued = 0;
+    if constexpr (LORA) {
+        // every tile of the first output slice reports a bad adapter, in whichever CTA it falls
+        for (int64_t i = tid; c0 + i * G < n_units; i += kPThreads) {
+            const PairTile un = pair_tile(c0 + i * G, n_pairs, n_ns);
+            const bool report = rank == 0 && un.ns == 0;
+            if (i < kPTable)
+                tab[i] = pair_lookup(p, un.pair, n_tiles, report);
+            else if (report)
+                pair_lookup(p, un.pair, n_tiles, true);
+        }
+        __syncthreads();
+    }
 
     if (warp == 0) {
         // ------------------------------------------------ producer (both CTAs)
-        int it = 0;
+        int it = 0, t = 0;
         if (p.test_stall)
             goto done;
         const uint64_t pol_x = policy_evict_first(), pol_w = policy_evict_last();
-        for (int64_t u = c0; u < n_units; u += G) {
+        for (int64_t u = c0; u < n_units; u += G, ++t) {
             const PairTile un = pair_tile(u, n_pairs, n_ns);
-            const PairRows pr = pair_rows<LORA>(p, un.pair, n_tiles, lane == 0 && un.ns == 0 && rank == 0);
-            const int n_all = pr.nf[0] + n_kb + pr.nf[1];
+            const PairRows pr = pair_rows<LORA>(p, tab, t, un.pair, n_tiles);
+            const int nf0 = LORA ? pr.nf(0) : 0, n_all = nf0 + n_kb + (LORA ? pr.nf(1) : 0);
             const int o0 = un.ns * BN + (int)rank * (BN / 2);
-            const int row = pr.row[rank];
+            const int row = rank ? pr.row[1] : pr.row[0];
             for (int k = 0; k < n_all; ++k, ++it) {
                 const int s = it % kStages;
                 if (!warp_wait(&empty_bar[s], ((it / kStages) & 1) ^ 1, &abort_flag, p.a.err, p.wait_ns))
                     goto done;
                 unsigned char *as = sm + s * kStage, *bs = as + kAtom;
-                const int kb = k - pr.nf[0];
+                const int kb = k - nf0;
                 const uint32_t bar = map_rank(smem_u32(&full_bar[s]), 0);
                 if (!LORA || (kb >= 0 && kb < n_kb)) {
                     if (lane == 0) {
                         if (rank == 0)
                             mbar_arrive_expect_tx(&full_bar[s], 2 * kStage);
-                        else if (LORA)
-                            remote_arrive(bar);
                         tma_load_pair(as, &p.map_q, bar, kb * kKB, row, pol_x);
                         tma_load_pair(bs, &p.map_w, bar, kb * kKB, o0, pol_w);
                     }
@@ -378,9 +381,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
                     // delta k-block j of a pass: part j % 2 (high, low) of rank columns 64 (j / 2) ..
                     const int pass = kb < 0 ? 0 : 1;
                     const int j = pass ? kb - n_kb : k;
-                    const PairAd ad = pass ? pr.ad[1] : pr.ad[0];
+                    const PairAd ad = pr.adapter(pass);
                     const int c = j >> 1, w = ad.r < 64 ? ad.r : 64;
-                    const bool mine = pr.same || pass == (int)rank;
+                    const bool mine = pr.same() || pass == (int)rank;
                     if (ad.m < 0) {
                         // no view of this rank: all lanes gather the CTA's BN / 2 output rows x 64
                         // rank columns (128-byte swizzle); past r and past d_out zeros
@@ -396,15 +399,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
                         __syncwarp();
                     }
                     if (lane == 0) {
+                        // (the s V boxes leave after the gather is complete in both CTAs, so
+                        // the barrier, which waits for both, covers the gathered rows too)
                         if (rank == 0)
                             mbar_arrive_expect_tx(&full_bar[s],
                                                   (uint32_t)(2 * (kAtom + (ad.m >= 0 ? BN / 2 * w * 2 : 0))));
-                        else
-                            remote_arrive(bar);
                         // (the other adapter's rows are never read, but a box has to arrive)
                         tma_load_pair(as, &p.map_v, bar, (j & 1) * p.a.kv + c * 64, mine ? row : p.a.N, pol_x);
                         if (ad.m >= 0)
-                            tma_load_pair(bs, &p.map_b[ad.m], bar, c * 64, ad.brow + o0, pol_w);
+                            tma_load_pair(bs, &p.map_b[ad.m], bar, c * 64, (int)(ad.boff >> (4 + ad.m)) + o0, pol_w);
                     }
                 }
                 __syncwarp();
@@ -413,26 +416,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader)
-        int it = 0, t = 0, fp = 0;
+        int it = 0, t = 0, pass_no = -1;
         const uint32_t idesc = idesc_i8(256, BN), idesc_f = idesc_bf16(256, BN);
         for (int64_t u = c0; u < n_units && rank == 0; u += G, ++t) {
             const PairTile un = pair_tile(u, n_pairs, n_ns);
-            const PairRows pr = pair_rows<LORA>(p, un.pair, n_tiles, false);
-            const int n_all = pr.nf[0] + n_kb + pr.nf[1];
-            const int b = t & 1;
+            const PairRows pr = pair_rows<LORA>(p, tab, t, un.pair, n_tiles);
+            const int nf0 = LORA ? pr.nf(0) : 0, n_all = nf0 + n_kb + (LORA ? pr.nf(1) : 0);
             for (int k = 0; k < n_all; ++k, ++it) {
                 const int s = it % kStages;
-                const int kb = k - pr.nf[0];
+                const int kb = k - nf0;
                 const bool base = !LORA || (kb >= 0 && kb < n_kb);
-                if (base && kb == 0 &&
-                    !pair_wait(&acc_empty[b], ((t >> 1) & 1) ^ 1, &abort_flag, p.a.err, p.wait_ns))
-                    goto done;
-                if (LORA && (k == 0 || kb == n_kb) && !base) {
-                    if (!pair_wait(&f_empty, (fp & 1) ^ 1, &abort_flag, p.a.err, p.wait_ns))
+                if (k == 0 || kb == n_kb) {          // a pass begins: its accumulators are free
+                    ++pass_no;
+                    if (!warp_wait(&acc_empty[pass_no % NB], ((pass_no / NB) & 1) ^ 1, &abort_flag, p.a.err, p.wait_ns))
                         goto done;
-                    ++fp;
                 }
-                if (!pair_wait(&full_bar[s], (it / kStages) & 1, &abort_flag, p.a.err, p.wait_ns))
+                const int b = pass_no % NB;
+                if (!warp_wait(&full_bar[s], (it / kStages) & 1, &abort_flag, p.a.err, p.wait_ns))
                     goto done;
                 tc_fence_after();
                 if (lane == 0) {
@@ -445,7 +445,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
                     } else {
                         const int pass = kb < 0 ? 0 : 1;
                         const int j = pass ? kb - n_kb : k;
-                        const PairAd ad = pass ? pr.ad[1] : pr.ad[0];
+                        const PairAd ad = pr.adapter(pass);
                         const int left = ad.r - (j >> 1) * 64;
                         const int steps = ((left < 64 ? left : 64) + 15) >> 4;
                         for (int i = 0; i < steps; ++i) {
@@ -457,10 +457,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
                         }
                     }
                     commit_pair(&empty_bar[s]);
-                    if (base && kb == n_kb - 1)
+                    if (kb == n_kb - 1 || k == n_all - 1)
                         commit_pair(&acc_full[b]);
-                    if (LORA && !base && (kb == -1 || k == n_all - 1))
-                        commit_pair(&f_full);
                 }
                 __syncwarp();
             }
@@ -470,73 +468,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
         const int q = warp & 3;                      // TMEM lane quarter
         const int half = (warp - 2) >> 2;            // columns [half * kCols, + kCols)
         const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + half * kCols;
-        int t = 0, fp = 0;
+        float *const sw = sw_tile[warp - 2];         // this warp's channel scales
+        int t = 0, pass_no = 0;
         for (int64_t u = c0; u < n_units; u += G, ++t) {
             const PairTile un = pair_tile(u, n_pairs, n_ns);
-            const PairRows pr = pair_rows<LORA>(p, un.pair, n_tiles, false);
-            const int b = t & 1, r = q * 32 + lane;
-            const int row = pr.row[rank] + r;
-            const bool valid = r < pr.cnt[rank];
+            const PairRows pr = pair_rows<LORA>(p, tab, t, un.pair, n_tiles);
+            const int r = q * 32 + lane;
+            const int row = (rank ? pr.row[1] : pr.row[0]) + r;
+            const bool valid = r < (rank ? pr.cnt[1] : pr.cnt[0]);
             const float sx = valid ? __ldg(p.a.Sx + row) : 0.f;
+            const int64_t yrow = (int64_t)row * p.a.ldy;
             const int o0 = un.ns * BN + half * kCols;
-            float f[LORA ? kCols : 1];
-            bool has_f = false;
-            if constexpr (LORA) {
+            for (int c = lane; c < kCols; c += 32)
+                sw[c] = o0 + c < p.a.d_out ? __ldg(p.a.Sw + o0 + c) : 0.f;
+            __syncwarp();
+            const int n_pass = LORA && pr.nf(1) ? 2 : 1;
 #pragma unroll 1
-                for (int pass = 0; pass < 2; ++pass) {
-                    if (pr.nf[pass] == 0)
-                        continue;
-                    if (!warp_wait(&f_full, fp & 1, &abort_flag, p.a.err, p.wait_ns))
-                        goto done;
-                    ++fp;
-                    tc_fence_after();
-                    if (pr.same || pass == (int)rank) {
-                        has_f = true;
+            for (int pass = 0; pass < n_pass; ++pass, ++pass_no) {
+                const int b = pass_no % NB;
+                if (!warp_wait(&acc_full[b], (pass_no / NB) & 1, &abort_flag, p.a.err, p.wait_ns))
+                    goto done;
+                tc_fence_after();
+                const uint32_t acc = lane_base + b * BN;
+                if constexpr (LORA) {
+                    const bool take = pass == (int)rank || n_pass == 1;
+                    const bool delta = (rank ? pr.ad[1] : pr.ad[0]) & 0xff;
+                    uint32_t out[kCols / 2];         // bf16 pairs
+                    if (take) {
 #pragma unroll
                         for (int c = 0; c < kCols; c += 16) {
-                            uint32_t w[16];
-                            tmem_ld16_raw(lane_base + kF + c, w);
+                            uint32_t w[16], f[16];
+                            tmem_ld16_raw(acc + c, w);
+                            if (delta)
+                                tmem_ld16_raw(acc + kF + c, f);
                             tmem_wait(w);
+                            tmem_wait(f);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                f[c + i] = __uint_as_float(w[i]);
+                            for (int i = 0; i < 16; i += 2) {
+                                float v0 = (float)(int)w[i] * (sx * sw[c + i]);
+                                float v1 = (float)(int)w[i + 1] * (sx * sw[c + i + 1]);
+                                if (delta) {
+                                    v0 += __uint_as_float(f[i]);
+                                    v1 += __uint_as_float(f[i + 1]);
+                                }
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
+                                out[(c + i) / 2] = *reinterpret_cast<const uint32_t *>(&h);
+                            }
                         }
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        remote_arrive(map_rank(smem_u32(&f_empty), 0));
-                }
-            }
-            if (!warp_wait(&acc_full[b], (t >> 1) & 1, &abort_flag, p.a.err, p.wait_ns))
-                goto done;
-            tc_fence_after();
-            const int64_t yrow = (int64_t)row * p.a.ldy;
+                        remote_arrive(map_rank(smem_u32(&acc_empty[b]), 0));
+                    if (take && valid) {
+                        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.a.Y) + yrow + o0;
 #pragma unroll
-            for (int c = 0; c < kCols; c += 16) {
-                uint32_t w[16];
-                tmem_ld16_raw(lane_base + b * BN + c, w);
-                tmem_wait(w);
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const int o = o0 + c + 8 * g;
-                    if (valid && o < p.a.d_out) {
-                        const float *sw = p.a.Sw + o;
-                        float v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            v[i] = (float)(int)w[8 * g + i] * (sx * __ldg(sw + i));
-                            if (LORA && has_f)
-                                v[i] += f[LORA ? c + 8 * g + i : 0];
-                        }
-                        store8(p.a.Y, p.a.dtype, yrow + o, v);
+                        for (int c = 0; c < kCols; c += 8)
+                            if (o0 + c < p.a.d_out)
+                                *reinterpret_cast<uint4 *>(y + c) =
+                                    make_uint4(out[c / 2], out[c / 2 + 1], out[c / 2 + 2], out[c / 2 + 3]);
                     }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kCols; c += kCols / 2) {
+                        uint32_t w[kCols / 2];
+                        tmem_ld16s(acc + c, w);
+                        tmem_wait(w);
+#pragma unroll
+                        for (int g = 0; g < kCols / 2; g += 8) {
+                            const int o = o0 + c + g;
+                            if (valid && o < p.a.d_out) {
+                                float v[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    v[i] = (float)(int)w[g + i] * (sx * sw[c + g + i]);
+                                store8(p.a.Y, p.a.dtype, yrow + o, v);
+                            }
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        remote_arrive(map_rank(smem_u32(&acc_empty[b]), 0));
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                remote_arrive(map_rank(smem_u32(&acc_empty[b]), 0));
         }
     }
 done:
