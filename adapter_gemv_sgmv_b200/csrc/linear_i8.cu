@@ -415,54 +415,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
             }
         }
     } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer (leader)
-        int it = 0, t = 0, pass_no = -1;
-        const uint32_t idesc = idesc_i8(256, BN), idesc_f = idesc_bf16(256, BN);
-        for (int64_t u = c0; u < n_units && rank == 0; u += G, ++t) {
-            const PairTile un = pair_tile(u, n_pairs, n_ns);
-            const PairRows pr = pair_rows<LORA>(p, tab, t, un.pair, n_tiles);
-            const int nf0 = LORA ? pr.nf(0) : 0, n_all = nf0 + n_kb + (LORA ? pr.nf(1) : 0);
-            for (int k = 0; k < n_all; ++k, ++it) {
-                const int s = it % kStages;
-                const int kb = k - nf0;
-                const bool base = !LORA || (kb >= 0 && kb < n_kb);
-                if (k == 0 || kb == n_kb) {          // a pass begins: its accumulators are free
-                    ++pass_no;
-                    if (!warp_wait(&acc_empty[pass_no % NB], ((pass_no / NB) & 1) ^ 1, &abort_flag, p.a.err, p.wait_ns))
-                        goto done;
+        // ------------------------------------------------ MMA issuer (leader, one thread)
+        // The loop is what feeds the tensor cores: with a warp-wide wait and addresses worked
+        // out per k-block it took 650 cycles for the 512 that a k-block's products take.
+        if (rank == 0 && lane == 0) {
+            const uint32_t idesc = idesc_i8(256, BN), idesc_f = idesc_bf16(256, BN);
+            const uint64_t a0 = sw128_desc(smem_u32(sm)), b0 = sw128_desc(smem_u32(sm) + kAtom);
+            int s = 0, t = 0, pass_no = 0;
+            uint32_t ph = 0;
+            auto next = [&] {
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1;
                 }
-                const int b = pass_no % NB;
-                if (!warp_wait(&full_bar[s], (it / kStages) & 1, &abort_flag, p.a.err, p.wait_ns))
-                    goto done;
-                tc_fence_after();
-                if (lane == 0) {
+            };
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return mbar_wait(bar, parity, &abort_flag, p.a.err, p.wait_ns);
+            };
+            auto delta = [&](const PairAd &ad, int nf) {
+                for (int j = 0; j < nf; ++j) {
+                    if (!wait(&full_bar[s], ph))
+                        return false;
+                    tc_fence_after();
                     const uint32_t as = smem_u32(sm + s * kStage), bs = as + kAtom;
-                    if (base) {
-#pragma unroll
-                        for (int i = 0; i < kKB / 32; ++i)
-                            mma_i8_pair(tmem + b * BN, sw128_desc(as + i * 32), sw128_desc(bs + i * 32), idesc,
-                                        (kb > 0 || i > 0) ? 1u : 0u);
-                    } else {
-                        const int pass = kb < 0 ? 0 : 1;
-                        const int j = pass ? kb - n_kb : k;
-                        const PairAd ad = pr.adapter(pass);
-                        const int left = ad.r - (j >> 1) * 64;
-                        const int steps = ((left < 64 ? left : 64) + 15) >> 4;
-                        for (int i = 0; i < steps; ++i) {
-                            // B columns in their view's swizzle
-                            const uint64_t bd = ad.r >= 64 || ad.m < 0 ? sw128_desc(bs + i * 32)
-                                              : (ad.r == 32 ? sw64_desc(bs + i * 32) : sw32_desc(bs));
-                            mma_bf16_pair(tmem + kF, sw128_desc(as + i * 32), bd, idesc_f,
-                                          (j > 0 || i > 0) ? 1u : 0u);
-                        }
+                    const int left = ad.r - (j >> 1) * 64;
+                    const int steps = ((left < 64 ? left : 64) + 15) >> 4;
+                    for (int i = 0; i < steps; ++i) {
+                        // B columns in their view's swizzle
+                        const uint64_t bd = ad.r >= 64 || ad.m < 0 ? sw128_desc(bs + i * 32)
+                                          : (ad.r == 32 ? sw64_desc(bs + i * 32) : sw32_desc(bs));
+                        mma_bf16_pair(tmem + kF, sw128_desc(as + i * 32), bd, idesc_f, (j > 0 || i > 0) ? 1u : 0u);
                     }
                     commit_pair(&empty_bar[s]);
-                    if (kb == n_kb - 1 || k == n_all - 1)
-                        commit_pair(&acc_full[b]);
+                    next();
                 }
-                __syncwarp();
+                return true;
+            };
+            for (int64_t u = c0; u < n_units; u += G, ++t) {
+                PairRows pr;
+                if constexpr (LORA)
+                    pr = pair_rows<LORA>(p, tab, t, pair_tile(u, n_pairs, n_ns).pair, n_tiles);
+                const int b = pass_no % NB;
+                if (!wait(&acc_empty[b], ((pass_no / NB) & 1) ^ 1))
+                    goto issued_all;
+                ++pass_no;
+                tc_fence_after();
+                if constexpr (LORA)
+                    if (!delta(pr.adapter(0), pr.nf(0)))
+                        goto issued_all;
+                const uint32_t d = tmem + b * BN;
+                for (int kb = 0; kb < n_kb; ++kb) {
+                    if (!wait(&full_bar[s], ph))
+                        goto issued_all;
+                    tc_fence_after();
+                    const uint64_t at = (uint64_t)(s * (kStage >> 4));
+#pragma unroll
+                    for (int i = 0; i < kKB / 32; ++i)
+                        mma_i8_pair(d, a0 + at + i * 2, b0 + at + i * 2, idesc, (kb > 0 || i > 0) ? 1u : 0u);
+                    commit_pair(&empty_bar[s]);
+                    next();
+                }
+                commit_pair(&acc_full[b]);
+                if constexpr (LORA) {
+                    if (pr.nf(1)) {                  // the second tile's own adapter
+                        if (!wait(&acc_empty[0], (pass_no & 1) ^ 1))
+                            goto issued_all;
+                        ++pass_no;
+                        tc_fence_after();
+                        if (!delta(pr.adapter(1), pr.nf(1)))
+                            goto issued_all;
+                        commit_pair(&acc_full[0]);
+                    }
+                }
             }
+        issued_all:;
         }
+        __syncwarp();
     } else {
         // ------------------------------------------------ epilogue (both CTAs)
         const int q = warp & 3;                      // TMEM lane quarter
