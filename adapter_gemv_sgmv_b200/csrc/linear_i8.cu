@@ -117,16 +117,18 @@ template <> struct PairCfg<false> {
     static constexpr int BN = 256, stages = 6, buffers = 2;
 };
 template <> struct PairCfg<true> {
-    static constexpr int BN = 256, stages = 6, buffers = 1;
+    static constexpr int BN = 256, stages = 5, buffers = 1;
 };
 
 struct PairTc {
     I8Args a;
     CUtensorMap map_q;       // tokens [N, d_in], boxes 128 bytes x 128 rows, 128-byte swizzle
     CUtensorMap map_w;       // weight [d_out, d_in], boxes 128 bytes x BN / 2 rows
+    CUtensorMap map_y;       // y [N, d_out], boxes 128 bytes x 32 rows (written)
     CUtensorMap map_v;       // LORA: s V as bf16 parts [N, 2 kv], boxes 64 columns x 128 rows
     CUtensorMap map_b[4];    // LORA: B pool as [B_elems / r, r], r = 16 << m, boxes of min(r, 64) x BN / 2 rows
     int32_t b_tma;
+    int32_t sw_vec;          // the channel scales may be read 16 bytes at a time
     unsigned long long wait_ns;
     int32_t test_stall;
 };
@@ -260,30 +262,58 @@ template <int N> __device__ __forceinline__ void tmem_wait(uint32_t (&r)[N])
         asm volatile("" : "+r"(r[i]));
 }
 
-// 8 scaled results to y
-__device__ __forceinline__ void store8(void *Y, int32_t dtype, int64_t at, const float (&v)[8])
+// two results as T, packed (fp32: the bits of one)
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16)
 {
-    if (dtype == LORA_F32) {
-        float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(Y) + at);
-        d[0] = make_float4(v[0], v[1], v[2], v[3]);
-        d[1] = make_float4(v[4], v[5], v[6], v[7]);
-        return;
-    }
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (dtype == LORA_BF16) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
-        } else {
-            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-    }
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(Y) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-template <bool LORA>
+// channel scales of outputs o .. o + 15 (zeros past d_out, a multiple of 8)
+__device__ __forceinline__ void load_sw(const PairTc &p, int o, float (&sw)[16])
+{
+#pragma unroll
+    for (int g = 0; g < 16; g += 8) {
+        const float *s = p.a.Sw + o + g;
+        if (o + g >= p.a.d_out) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                sw[g + i] = 0.f;
+        } else if (p.sw_vec) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+                const float4 v = __ldg(reinterpret_cast<const float4 *>(s + i));
+                sw[g + i] = v.x;
+                sw[g + i + 1] = v.y;
+                sw[g + i + 2] = v.z;
+                sw[g + i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                sw[g + i] = __ldg(s + i);
+        }
+    }
+}
+
+// A warp's box of 32 rows x 128 bytes in shared memory to y; the box may be written again
+// after box_free().
+__device__ __forceinline__ void box_store(const CUtensorMap *map, const void *box, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
+                 ::"l"(map), "r"(smem_u32(box)), "r"(x), "r"(y)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void box_free() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void box_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+template <bool LORA, class T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_pair(const __grid_constant__ PairTc p)
 {
     using C = PairCfg<LORA>;
@@ -298,7 +328,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
     __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
     __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], mma_drain;
     __shared__ PairRows tab[LORA ? kPTable : 1];
-    __shared__ __align__(16) float sw_tile[kPEpiWarps][kCols];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
 
@@ -496,7 +525,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
         const int q = warp & 3;                      // TMEM lane quarter
         const int half = (warp - 2) >> 2;            // columns [half * kCols, + kCols)
         const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + half * kCols;
-        float *const sw = sw_tile[warp - 2];         // this warp's channel scales
+        unsigned char *const box = sm + kStages * kStage + (warp - 2) * 4096;    // 32 rows x 128 bytes
+        constexpr int kBoxCols = 128 / sizeof(T);
         int t = 0, pass_no = 0;
         for (int64_t u = c0; u < n_units; u += G, ++t) {
             const PairTile un = pair_tile(u, n_pairs, n_ns);
@@ -505,11 +535,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
             const int row = (rank ? pr.row[1] : pr.row[0]) + r;
             const bool valid = r < (rank ? pr.cnt[1] : pr.cnt[0]);
             const float sx = valid ? __ldg(p.a.Sx + row) : 0.f;
-            const int64_t yrow = (int64_t)row * p.a.ldy;
+            const int row0 = row - lane;             // the warp's first row
             const int o0 = un.ns * BN + half * kCols;
-            for (int c = lane; c < kCols; c += 32)
-                sw[c] = o0 + c < p.a.d_out ? __ldg(p.a.Sw + o0 + c) : 0.f;
-            __syncwarp();
             const int n_pass = LORA && pr.nf(1) ? 2 : 1;
 #pragma unroll 1
             for (int pass = 0; pass < n_pass; ++pass, ++pass_no) {
@@ -526,21 +553,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
 #pragma unroll
                         for (int c = 0; c < kCols; c += 16) {
                             uint32_t w[16], f[16];
+                            float sw[16];
                             tmem_ld16_raw(acc + c, w);
                             if (delta)
                                 tmem_ld16_raw(acc + kF + c, f);
+                            load_sw(p, o0 + c, sw);
                             tmem_wait(w);
                             tmem_wait(f);
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
-                                float v0 = (float)(int)w[i] * (sx * sw[c + i]);
-                                float v1 = (float)(int)w[i + 1] * (sx * sw[c + i + 1]);
+                                float v0 = (float)(int)w[i] * (sx * sw[i]);
+                                float v1 = (float)(int)w[i + 1] * (sx * sw[i + 1]);
                                 if (delta) {
                                     v0 += __uint_as_float(f[i]);
                                     v1 += __uint_as_float(f[i + 1]);
                                 }
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
-                                out[(c + i) / 2] = *reinterpret_cast<const uint32_t *>(&h);
+                                out[(c + i) / 2] = pack2(v0, v1, T());
                             }
                         }
                     }
@@ -548,8 +576,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
                     __syncwarp();
                     if (lane == 0)
                         remote_arrive(map_rank(smem_u32(&acc_empty[b]), 0));
-                    if (take && valid) {
-                        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.a.Y) + yrow + o0;
+                    if (take && __all_sync(0xffffffffu, valid)) {
+#pragma unroll
+                        for (int c = 0; c < kCols; c += kBoxCols) {
+                            if (lane == 0)
+                                box_free();
+                            __syncwarp();
+#pragma unroll
+                            for (int g = 0; g < 8; ++g)
+                                st_shared_v4(smem_u32(box) + sw128_off(lane, g), out[c / 2 + 4 * g], out[c / 2 + 4 * g + 1],
+                                             out[c / 2 + 4 * g + 2], out[c / 2 + 4 * g + 3]);
+                            fence_async_smem();
+                            __syncwarp();
+                            if (lane == 0 && o0 + c < p.a.d_out)
+                                box_store(&p.map_y, box, o0 + c, row0);
+                        }
+                    } else if (take && valid) {      // a segment's last rows: what follows is not ours
+                        T *y = static_cast<T *>(p.a.Y) + (int64_t)row * p.a.ldy + o0;
 #pragma unroll
                         for (int c = 0; c < kCols; c += 8)
                             if (o0 + c < p.a.d_out)
@@ -557,33 +600,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
                                     make_uint4(out[c / 2], out[c / 2 + 1], out[c / 2 + 2], out[c / 2 + 3]);
                     }
                 } else {
-#pragma unroll
-                    for (int c = 0; c < kCols; c += kCols / 2) {
-                        uint32_t w[kCols / 2];
+#pragma unroll 1
+                    for (int c = 0; c < kCols; c += kBoxCols) {
+                        uint32_t w[kBoxCols];
                         tmem_ld16s(acc + c, w);
+                        if (lane == 0)
+                            box_free();
                         tmem_wait(w);
+                        if (c + kBoxCols == kCols) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                remote_arrive(map_rank(smem_u32(&acc_empty[b]), 0));
+                        }
+                        __syncwarp();
 #pragma unroll
-                        for (int g = 0; g < kCols / 2; g += 8) {
-                            const int o = o0 + c + g;
-                            if (valid && o < p.a.d_out) {
-                                float v[8];
+                        for (int g = 0; g < kBoxCols; g += 16) {
+                            float sw[16], v[16];
+                            load_sw(p, o0 + c + g, sw);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    v[i] = (float)(int)w[g + i] * (sx * sw[c + g + i]);
-                                store8(p.a.Y, p.a.dtype, yrow + o, v);
+                            for (int i = 0; i < 16; ++i)
+                                v[i] = (float)(int)w[g + i] * (sx * sw[i]);
+                            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4)
+                                    st_shared_v4(smem_u32(box) + sw128_off(lane, (g + i) / 4), __float_as_uint(v[i]),
+                                                 __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
+                                                 __float_as_uint(v[i + 3]));
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 16; i += 8)
+                                    st_shared_v4(smem_u32(box) + sw128_off(lane, (g + i) / 8), pack2(v[i], v[i + 1], T()),
+                                                 pack2(v[i + 2], v[i + 3], T()), pack2(v[i + 4], v[i + 5], T()),
+                                                 pack2(v[i + 6], v[i + 7], T()));
                             }
                         }
+                        fence_async_smem();
+                        __syncwarp();
+                        // (rows past N and outputs past d_out are clipped by the map)
+                        if (lane == 0 && row0 < p.a.N && o0 + c < p.a.d_out)
+                            box_store(&p.map_y, box, o0 + c, row0);
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        remote_arrive(map_rank(smem_u32(&acc_empty[b]), 0));
                 }
             }
         }
     }
 done:
     __syncwarp();
+    box_done();                                      // y is written, the boxes are read
     // nothing may land in shared memory or TMEM, or be read by the pair's MMAs, after
     // either CTA lets go of them
     if (warp == 0 && rank == 0)
@@ -608,6 +672,23 @@ done:
     }
 }
 
+bool encode_y(CUtensorMap *m, void *Y, int32_t dtype, int64_t rows, int64_t cols, int64_t ld)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return false;
+    const int es = dtype == LORA_F32 ? 4 : 2;
+    const CUtensorMapDataType t = dtype == LORA_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : dtype == LORA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * es};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / es), 32};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, t, 2, Y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Row-major 8-bit matrix [rows, cols] with leading dimension ld: boxes of 128 bytes x
 // box_rows rows, 128-byte swizzle, zeros outside the matrix.
 bool encode_box8(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld, int box_rows)
@@ -624,12 +705,14 @@ bool encode_box8(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool LORA> cudaError_t launch_pair(const I8Args &a, int64_t max_tiles, cudaStream_t s, bool *ok)
+template <bool LORA, class T> cudaError_t launch_pair(const I8Args &a, int64_t max_tiles, cudaStream_t s, bool *ok)
 {
     using C = PairCfg<LORA>;
     PairTc p = {};
     p.a = a;
-    *ok = encode_box8(&p.map_q, a.Q, a.N, a.d_in, a.ldq, 128) && encode_box8(&p.map_w, a.W, a.d_out, a.d_in, a.ldw, C::BN / 2);
+    *ok = encode_box8(&p.map_q, a.Q, a.N, a.d_in, a.ldq, 128) && encode_box8(&p.map_w, a.W, a.d_out, a.d_in, a.ldw, C::BN / 2) &&
+          encode_y(&p.map_y, a.Y, a.dtype, a.N, a.d_out, a.ldy);
+    p.sw_vec = ((uintptr_t)a.Sw & 15) == 0;
     if (*ok && LORA) {
         *ok = encode_box(&p.map_v, a.Vb, a.N, 2 * (int64_t)a.kv, a.ldvb, 128);
         p.b_tma = encode_b_views(p.map_b, a.pool.B, a.pool.B_elems, C::BN / 2);
@@ -638,14 +721,14 @@ template <bool LORA> cudaError_t launch_pair(const I8Args &a, int64_t max_tiles,
         return cudaSuccess;
     p.wait_ns = wait_bound_ns();
     p.test_stall = test_stall_mode();
-    const int smem = C::stages * (kAtom + C::BN / 2 * 128) + 1024;
+    const int smem = C::stages * (kAtom + C::BN / 2 * 128) + kPEpiWarps * 4096 + 1024;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        if ((e = cudaFuncSetAttribute(k_i8_pair<LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+        if ((e = cudaFuncSetAttribute(k_i8_pair<LORA, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
             return e;
         if (dev >= 0 && dev < 64)
             attr_set[dev] = true;
@@ -665,14 +748,18 @@ template <bool LORA> cudaError_t launch_pair(const I8Args &a, int64_t max_tiles,
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_i8_pair<LORA>, p);
+    return cudaLaunchKernelEx(&cfg, k_i8_pair<LORA, T>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_i8(const I8Args &a, int max_tiles, cudaStream_t s, bool *ok)
 {
-    return a.groups ? launch_pair<true>(a, max_tiles, s, ok) : launch_pair<false>(a, 0, s, ok);
+    if (a.groups)
+        return launch_pair<true, __nv_bfloat16>(a, max_tiles, s, ok);
+    return a.dtype == LORA_BF16 ? launch_pair<false, __nv_bfloat16>(a, 0, s, ok)
+         : a.dtype == LORA_F16 ? launch_pair<false, __half>(a, 0, s, ok)
+                               : launch_pair<false, float>(a, 0, s, ok);
 }
 
 }  // namespace lora
