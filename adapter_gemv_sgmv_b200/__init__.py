@@ -389,109 +389,111 @@ def lora_linear_sgmv(X, W, Y, pool, seg_off, seg_ad, scale: float, ws: Workspace
     return ws
 
 
-_DTYPES = {"torch.bfloat16": 0, "torch.float16": 1, "torch.float32": 2}      # lora_dtype
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+_dtype_codes: dict = {}                                # torch dtype -> lora_dtype
 
 
 def _dtype(t, name: str) -> int:
-    code = _DTYPES.get(str(t.dtype))
+    if not _dtype_codes:
+        torch = _torch()
+        _dtype_codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    code = _dtype_codes.get(t.dtype)
     if code is None:
         raise LoraError(f"{name} must be bf16, fp16 or fp32", 2)
     return code
 
 
-def _rows(t, name: str, dtypes=None):
+def _rows(t, name: str, dtype=None):
     """Leading dimension of a 2-D tensor of rows (a single row has none: any that fits will do)."""
-    if t.dim() != 2 or (dtypes and str(t.dtype) not in dtypes) or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2 or (dtype is not None and t.dtype != dtype) or (t.stride(1) != 1 and t.shape[1] > 1):
         raise LoraError(f"{name} must be a 2-D tensor with unit-stride columns", 1)
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+    n, d = t.shape
+    return t.stride(0) if n > 1 else (d + 15) // 16 * 16
 
 
 def _vec(t, n: int, name: str):
-    if str(t.dtype) != "torch.float32" or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.dtype != _torch().float32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
         raise LoraError(f"{name} must be a contiguous fp32 tensor of {n} scales", 1)
 
 
-class _Launch:
-    """The stream of a call and, where the tensors live on another device than the current
-    one, that device made current for its duration (a launch goes to the current device)."""
-
-    def __init__(self, stream, *tensors):
-        torch = _torch()
-        _check_dev(*tensors)
-        dev = tensors[0].device
-        if any(t.device != dev for t in tensors):
+def _device_index(*tensors) -> int:
+    """The one CUDA device the tensors live on."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev or not t.is_cuda:
             raise LoraError("tensors must live on one CUDA device", 1)
-        self.device = dev
-        self._guard = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
-        self._given = stream
-        self.stream = int((stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream)
+    return dev
 
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self
 
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-        return False
-
-    def workspace(self, nbytes: int) -> Workspace:
-        """A workspace of this device and stream: calls on two streams never share one.  Under
-        graph capture it is a fresh one from the graph's memory, so that no two graphs share it."""
-        torch = _torch()
-        if self._given is not None:                    # allocated, and freed, in that stream's order
-            with torch.cuda.stream(self._given):
-                return self._workspace(nbytes)
-        return self._workspace(nbytes)
-
-    def _workspace(self, nbytes: int) -> Workspace:
-        if _torch().cuda.is_current_stream_capturing():
-            return Workspace(nbytes, device=self.device)
-        key = (self.device.index, self.stream)
-        ws = _stream_ws.get(key)
-        if ws is None or ws.nbytes < nbytes:
-            ws = _stream_ws[key] = Workspace(max(nbytes, 2 * (ws.nbytes if ws else 0)), device=self.device)
-        return ws
+def _on_device(dev: int, stream, call):
+    """call(raw stream) with `dev` current: a launch goes to the current device, which need
+    not be the tensors'.  Without a stream, that device's current one."""
+    torch = _torch()
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
+    if torch._C._cuda_getDevice() == dev:
+        return call(raw)
+    with torch.cuda.device(dev):
+        return call(raw)
 
 
 _stream_ws: dict = {}
 
 
+def _stream_workspace(nbytes: int, dev: int, raw: int, stream) -> Workspace:
+    """A workspace of this device and stream: calls on two streams never share one.  Under graph
+    capture it is a fresh one from the graph's memory, so that no two graphs share it."""
+    torch = _torch()
+    if stream is not None and raw != torch._C._cuda_getCurrentRawStream(dev):
+        with torch.cuda.stream(stream):                # allocated, and freed, in that stream's order
+            return _stream_workspace(nbytes, dev, raw, stream)
+    if torch.cuda.is_current_stream_capturing():
+        return Workspace(nbytes, device=torch.device("cuda", dev))
+    ws = _stream_ws.get((dev, raw))
+    if ws is None or ws.nbytes < nbytes:
+        ws = _stream_ws[dev, raw] = Workspace(max(nbytes, 2 * (ws.nbytes if ws else 0)),
+                                              device=torch.device("cuda", dev))
+    return ws
+
+
 def lora_quant_i8(X, Q, S, stream=None):
     """Q[n] = round(127 X[n] / max|X[n]|) (int8), S[n] = max|X[n]| / 127 for rows of bf16, fp16 or fp32."""
     lib = load()
-    with _Launch(stream, X, Q, S) as la:
-        ldx, ldq = _rows(X, "X"), _rows(Q, "Q", ("torch.int8",))
-        if tuple(Q.shape) != tuple(X.shape):
-            raise LoraError("Q must have X's shape", 1)
-        _vec(S, X.shape[0], "S")
-        _rc(lib.lora_quant_i8(_ptr(X), _dtype(X, "X"), ldx, _ptr(Q), ldq, _ptr(S), int(X.shape[0]),
-                              int(X.shape[1]), la.stream), "lora_quant_i8")
+    dev = _device_index(X, Q, S)
+    ldx, ldq = _rows(X, "X"), _rows(Q, "Q", _torch().int8)
+    if Q.shape != X.shape:
+        raise LoraError("Q must have X's shape", 1)
+    n, d = X.shape
+    _vec(S, n, "S")
+    dt = _dtype(X, "X")
+    _rc(_on_device(dev, stream, lambda raw: lib.lora_quant_i8(
+        X.data_ptr(), dt, ldx, Q.data_ptr(), ldq, S.data_ptr(), n, d, raw)), "lora_quant_i8")
 
 
 def _i8_operands(Q, Sx, Wq, Sw, Y):
-    ldq, ldw = _rows(Q, "Q", ("torch.int8",)), _rows(Wq, "Wq", ("torch.int8",))
-    ldy = _rows(Y, "Y")
-    N, d_in, d_out = int(Q.shape[0]), int(Q.shape[1]), int(Wq.shape[0])
-    if int(Wq.shape[1]) != d_in or tuple(Y.shape) != (N, d_out):
+    i8 = _torch().int8
+    ldq, ldw, ldy = _rows(Q, "Q", i8), _rows(Wq, "Wq", i8), _rows(Y, "Y")
+    (n, d_in), d_out = Q.shape, Wq.shape[0]
+    if Wq.shape[1] != d_in or Y.shape[0] != n or Y.shape[1] != d_out:
         raise LoraError("Q [N, d_in], Wq [d_out, d_in] and Y [N, d_out] do not fit together", 1)
-    _vec(Sx, N, "Sx")
+    _vec(Sx, n, "Sx")
     _vec(Sw, d_out, "Sw")
-    return ldq, ldw, ldy, N, d_in, d_out
+    return ldq, ldw, ldy, n, d_in, d_out
 
 
 def lora_linear_i8(Q, Sx, Wq, Sw, Y, ws: Workspace | None = None, stream=None):
     """Y[n][o] = Sx[n] Sw[o] sum_i Q[n][i] Wq[o][i] for int8 tokens and weight; Y is bf16, fp16 or
     fp32 and overwritten.  Returns the workspace (its error word: lora_get_error)."""
     lib = load()
-    with _Launch(stream, Q, Sx, Wq, Sw, Y) as la:
-        ldq, ldw, ldy, N, d_in, d_out = _i8_operands(Q, Sx, Wq, Sw, Y)
-        ws = ws or la.workspace(256)
-        _rc(lib.lora_linear_i8(_ptr(Q), ldq, _ptr(Sx), _ptr(Wq), ldw, _ptr(Sw), _ptr(Y), _dtype(Y, "Y"), ldy, N,
-                               d_in, d_out, ws.ptr(), ws.nbytes, la.stream), "lora_linear_i8")
-    return ws
+    dev = _device_index(Q, Sx, Wq, Sw, Y)
+    ldq, ldw, ldy, n, d_in, d_out = _i8_operands(Q, Sx, Wq, Sw, Y)
+    dt = _dtype(Y, "Y")
+
+    def call(raw):
+        w = ws or _stream_workspace(256, dev, raw, stream)
+        _rc(lib.lora_linear_i8(Q.data_ptr(), ldq, Sx.data_ptr(), Wq.data_ptr(), ldw, Sw.data_ptr(), Y.data_ptr(), dt,
+                               ldy, n, d_in, d_out, w.ptr(), w.nbytes, raw), "lora_linear_i8")
+        return w
+    return _on_device(dev, stream, call)
 
 
 def lora_linear_i8_sgmv(Q, Sx, X, Wq, Sw, Y, pool, seg_off, seg_ad, scale: float, ws: Workspace | None = None,
@@ -502,23 +504,28 @@ def lora_linear_i8_sgmv(Q, Sx, X, Wq, Sw, Y, pool, seg_off, seg_ad, scale: float
     the segments and left alone outside them."""
     lib = load()
     torch = _torch()
-    with _Launch(stream, Q, Sx, X, Wq, Sw, Y, seg_off, seg_ad, pool.A, pool.B) as la:
-        ldq, ldw, ldy, N, d_in, d_out = _i8_operands(Q, Sx, Wq, Sw, Y)
-        ps = make_pool_struct(pool, max_rank)
-        _mat(Y, ps.d_out, "Y")
-        ldx = _mat(X, ps.d_in, "X")
-        if d_in != ps.d_in or int(X.shape[0]) != N:
-            raise LoraError("Q, X and the pool disagree on N or d_in", 1)
-        n_seg = int(seg_ad.numel())
-        for t, n, name in ((seg_off, n_seg + 1, "seg_off"), (seg_ad, n_seg, "seg_ad")):
-            if t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous():
-                raise LoraError(f"{name} must be a contiguous int32 tensor of {n} entries", 1)
-        need = lora_workspace_size(OP_LINEAR_I8_SGMV, N, ps.n_adapters, ps.d_in, ps.d_out, ps.max_rank, n_seg)
-        ws = ws or la.workspace(need)
-        _rc(lib.lora_linear_i8_sgmv(_ptr(Q), ldq, _ptr(Sx), _ptr(X), ldx, _ptr(Wq), ldw, _ptr(Sw), _ptr(Y), ldy,
-                                    ctypes.byref(ps), _ptr(seg_off), _ptr(seg_ad), n_seg, N, float(scale),
-                                    ws.ptr(), ws.nbytes, la.stream), "lora_linear_i8_sgmv")
-    return ws
+    dev = _device_index(Q, Sx, X, Wq, Sw, Y, seg_off, seg_ad, pool.A, pool.B, pool.A_off, pool.B_off, pool.rank)
+    ldq, ldw, ldy, n, d_in, d_out = _i8_operands(Q, Sx, Wq, Sw, Y)
+    ps = make_pool_struct(pool, max_rank)
+    ldx = _rows(X, "X", torch.bfloat16)
+    if Y.dtype != torch.bfloat16:
+        raise LoraError("Y must be bf16", 1)
+    if d_in != ps.d_in or d_out != ps.d_out or X.shape != Q.shape:
+        raise LoraError("Q, X, Wq and the pool disagree on N, d_in or d_out", 1)
+    n_seg = seg_ad.numel()
+    for t, need, name in ((seg_off, n_seg + 1, "seg_off"), (seg_ad, n_seg, "seg_ad")):
+        if t.dtype != torch.int32 or t.numel() < need or not t.is_contiguous():
+            raise LoraError(f"{name} must be a contiguous int32 tensor of {need} entries", 1)
+
+    def call(raw):
+        w = ws or _stream_workspace(lora_workspace_size(OP_LINEAR_I8_SGMV, n, ps.n_adapters, d_in, d_out, ps.max_rank,
+                                                        n_seg), dev, raw, stream)
+        _rc(lib.lora_linear_i8_sgmv(Q.data_ptr(), ldq, Sx.data_ptr(), X.data_ptr(), ldx, Wq.data_ptr(), ldw,
+                                    Sw.data_ptr(), Y.data_ptr(), ldy, ctypes.byref(ps), seg_off.data_ptr(),
+                                    seg_ad.data_ptr(), n_seg, n, float(scale), w.ptr(), w.nbytes, raw),
+            "lora_linear_i8_sgmv")
+        return w
+    return _on_device(dev, stream, call)
 
 
 def lora_rope(xs, ys, pos, freqs, interleaved: bool = False, mscale: float = 1.0, inverse: bool = False,
@@ -529,26 +536,33 @@ def lora_rope(xs, ys, pos, freqs, interleaved: bool = False, mscale: float = 1.0
     [rot / 2] on the device, rot <= dim; pos: int32 or int64 [N].  `inverse` turns back: the gradient."""
     lib = load()
     torch = _torch()
-    xs, ys = list(xs), list(ys)
-    if not xs or len(xs) != len(ys):
+    k = len(xs)
+    if k == 0 or k != len(ys):
         raise LoraError("one output per input", 1)
-    with _Launch(stream, *xs, *ys, pos, freqs) as la:
-        n, dim = (int(xs[0].shape[0]), int(xs[0].shape[2])) if xs[0].dim() == 3 else (0, 0)
-        for x, y in zip(xs, ys):
-            if (x.dim() != 3 or x.shape != y.shape or x.dtype != y.dtype or x.dtype != xs[0].dtype or
-                    int(x.shape[0]) != n or int(x.shape[2]) != dim or x.stride(2) != 1 or y.stride(2) != 1):
-                raise LoraError("tensors [N, heads, dim] of one type, N and dim, unit stride inside a head", 1)
-        if pos.dtype not in (torch.int32, torch.int64) or pos.dim() != 1 or int(pos.shape[0]) != n or (
-                n > 1 and pos.stride(0) != 1):
-            raise LoraError("pos must be a contiguous int32 or int64 tensor [N]", 1)
-        if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
-            raise LoraError("freqs must be a contiguous fp64 tensor [rot / 2]", 1)
-        mats = (LoraRopeMat * len(xs))(*[
-            LoraRopeMat(_ptr(x), _ptr(y), x.stride(0), x.stride(1), y.stride(0), y.stride(1), int(x.shape[1]))
-            for x, y in zip(xs, ys)])
-        _rc(lib.lora_rope(mats, len(xs), _dtype(xs[0], "x"), _ptr(pos), pos.element_size(), _ptr(freqs), n, dim,
-                          2 * int(freqs.numel()), int(bool(interleaved)), int(bool(inverse)), float(mscale),
-                          la.stream), "lora_rope")
+    dev = _device_index(pos, freqs, *xs, *ys)
+    x0 = xs[0]
+    if x0.dim() != 3:
+        raise LoraError("tensors must be [N, heads, dim]", 1)
+    n, _, dim = x0.shape
+    mats = (LoraRopeMat * k)()
+    for m, x, y in zip(mats, xs, ys):
+        if (x.dim() != 3 or x.shape != y.shape or x.dtype != x0.dtype or y.dtype != x0.dtype or x.shape[0] != n or
+                x.shape[2] != dim):
+            raise LoraError("tensors [N, heads, dim] of one type, N and dim", 1)
+        m.x_token, m.x_head, sx = x.stride()
+        m.y_token, m.y_head, sy = y.stride()
+        if sx != 1 or sy != 1:
+            raise LoraError("unit stride inside a head", 1)
+        m.x, m.y, m.heads = x.data_ptr(), y.data_ptr(), x.shape[1]
+    if pos.dtype not in (torch.int32, torch.int64) or pos.dim() != 1 or pos.shape[0] != n or (
+            n > 1 and pos.stride(0) != 1):
+        raise LoraError("pos must be a contiguous int32 or int64 tensor [N]", 1)
+    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise LoraError("freqs must be a contiguous fp64 tensor [rot / 2]", 1)
+    dt = _dtype(x0, "x")
+    _rc(_on_device(dev, stream, lambda raw: lib.lora_rope(
+        mats, k, dt, pos.data_ptr(), pos.element_size(), freqs.data_ptr(), n, dim, 2 * freqs.shape[0],
+        1 if interleaved else 0, 1 if inverse else 0, mscale, raw)), "lora_rope")
 
 
 def lora_rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, low: float = 1.0,
