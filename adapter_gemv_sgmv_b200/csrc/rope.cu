@@ -13,9 +13,10 @@
 // reduced angle goes to sincospif in fp32.  cos and sin carry m; the products are fp32,
 // each output is rounded to its type once.
 //
-// Bound: HBM, one read and one write per element.  A block takes one token (several
-// where a token has few heads): its cos / sin come out once, in shared memory, for all
-// heads, and each thread's loads of x are in flight while they are computed.
+// Bound: HBM, one read and one write per element.  A block takes up to 8 tokens: their
+// cos / sin come out once, in shared memory, for all heads, while the first loads of x
+// are in flight.  17389 tokens of 32 + 8 heads of 128 in bf16 (356 MB): 65 us, 5.4 TB/s;
+// with one token a block, its angles' latency in every token's way, 113 us.
 
 #include "lora_internal.cuh"
 
@@ -27,14 +28,14 @@ namespace lora {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeHold = 2;        // items a thread loads ahead of the angles
+constexpr int kRopeHold = 2;        // items a thread has in flight
 
 struct RopeMat {
     const void *x;
     void *y;
     int64_t xs, xh, ys, yh;         // token and head strides, elements
-    int32_t heads;
-    int32_t first;                  // items of a token before this matrix's
+    int32_t first;                  // this matrix's first head among the token's heads
+    int32_t pad;
 };
 
 struct RopeArgs {
@@ -44,21 +45,32 @@ struct RopeArgs {
     int32_t pos64;
     const double *freq;
     int32_t N, dim, half;           // half = rot / 2
+    int32_t heads;                  // of a token, all matrices
     int32_t rot_items, head_items;  // items of a head that rotate; all of them
-    int32_t items;                  // of a token
+    int32_t cols, slots;            // threads along a head's items, and along heads
     int32_t tokens;                 // per block
     float m;
     float sign;                     // -1: inverse
 };
 
-// V elements at p as fp32
-template <class T, int V> __device__ __forceinline__ void get(const T *p, float (&f)[V])
+// V elements as loaded (16 bytes, or one element)
+template <class T, int V> struct Raw { uint4 u; };
+template <class T> struct Raw<T, 1> { T u; };
+
+template <class T, int V> __device__ __forceinline__ void get(const T *p, Raw<T, V> &r)
+{
+    if constexpr (V == 1)
+        r.u = *p;
+    else
+        r.u = *reinterpret_cast<const uint4 *>(p);
+}
+
+template <class T, int V> __device__ __forceinline__ void widen(const Raw<T, V> &r, float *f)
 {
     if constexpr (V == 1) {
-        f[0] = (float)p[0];
+        f[0] = (float)r.u;
     } else {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (std::is_same<T, float>::value) {
@@ -75,7 +87,7 @@ template <class T, int V> __device__ __forceinline__ void get(const T *p, float 
     }
 }
 
-template <class T, int V> __device__ __forceinline__ void put(T *p, const float (&f)[V])
+template <class T, int V> __device__ __forceinline__ void put(T *p, const float *f)
 {
     if constexpr (V == 1) {
         if constexpr (std::is_same<T, float>::value)
@@ -102,130 +114,125 @@ template <class T, int V> __device__ __forceinline__ void put(T *p, const float 
     }
 }
 
-// An item: V pairs of one head (two runs of V elements; interleaved: one run of V
-// elements, or a single pair where V is 1), or a run of V copied from past rot.
-template <class T, int V, bool INTER> struct Item {
-    static constexpr int U = INTER && V == 1 ? 2 : V;
-    const T *x;
-    T *y;
-    int pair;             // first pair's place in the block's cos / sin; -1: copy
-    float a[U], b[INTER ? 1 : U];
-};
-
+// An item is V pairs of one head (two runs of V elements half a rotation apart;
+// interleaved: one run of V elements, or a single pair where V is 1), or, past rot, a run
+// of V elements that is copied.  A thread keeps its place c along a head's items and
+// walks the block's (token, head) list, so no index is divided on the way; kRopeHold
+// items are in flight at a time, the first ones while the angles are worked out.
 template <class T, int V, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ RopeArgs p)
 {
     extern __shared__ float2 cs[];                   // [tokens][half]
-    using It = Item<T, V, INTER>;
-    constexpr int U = It::U;
+    constexpr bool kTwo = !INTER || V == 1;          // an item has a second run
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, nt = blockDim.x;
+    const int tid = threadIdx.x;
     const int n0 = blockIdx.x * p.tokens;
     const int n_tok = min(p.tokens, p.N - n0);
-    const int total = n_tok * p.items;
+    const int slot = tid / p.cols, c_first = tid - slot * p.cols;
+    const int dt = p.slots / p.heads, dh = p.slots - dt * p.heads;    // a step along the list
 
-    auto load = [&](int i, It &it) {
-        const int t = i / p.items;
-        int k = i - t * p.items;
+    struct Item {
+        T *y;
+        int t;                                       // token of the block, -1: no item
+        Raw<T, V> a, b;
+    };
+    auto fetch = [&](Item &it, int t, int h, int e, bool two) {
+        it.t = t < n_tok ? t : -1;
+        if (t >= n_tok)
+            return;
         int q = 0;
 #pragma unroll
         for (int j = 1; j < LORA_MAX_PROJ; ++j)
-            if (j < p.n_mat && k >= p.mat[j].first)
+            if (j < p.n_mat && h >= p.mat[j].first)
                 q = j;
-        k -= p.mat[q].first;
-        const int h = k / p.head_items, c = k - h * p.head_items;
-        const int64_t n = n0 + t;
-        it.x = static_cast<const T *>(p.mat[q].x) + n * p.mat[q].xs + h * p.mat[q].xh;
-        it.y = static_cast<T *>(p.mat[q].y) + n * p.mat[q].ys + h * p.mat[q].yh;
-        if (c < p.rot_items) {
-            const int e = INTER ? c * U : c * V;     // first element
-            it.pair = t * p.half + (INTER ? e / 2 : e);
-            it.x += e;
-            it.y += e;
-            if constexpr (V == 1) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    it.a[u] = (float)it.x[u];
-            } else {
-                get<T, V>(it.x, it.a);
-            }
-            if constexpr (!INTER)
-                get<T, V>(it.x + p.half, it.b);
-        } else {
-            const int e = 2 * p.half + (c - p.rot_items) * V;
-            it.pair = -1;
-            it.x += e;
-            it.y += e;
-            if constexpr (V == 1)
-                it.a[0] = (float)it.x[0];
-            else
-                get<T, V>(it.x, it.a);
-        }
+        const RopeMat &m = p.mat[q];
+        const int64_t n = n0 + t, hh = h - m.first;
+        const T *x = static_cast<const T *>(m.x) + n * m.xs + hh * m.xh + e;
+        it.y = static_cast<T *>(m.y) + n * m.ys + hh * m.yh + e;
+        get<T, V>(x, it.a);
+        if (kTwo && two)
+            get<T, V>(x + (INTER ? 1 : p.half), it.b);
     };
-    auto store = [&](It &it) {
-        if (it.pair < 0) {
-            if constexpr (V == 1) {
-                float f[1] = {it.a[0]};
-                put<T, 1>(it.y, f);
-            } else {
-                put<T, V>(it.y, it.a);
-            }
+    auto finish = [&](const Item &it, int pair, bool rotate) {
+        if (it.t < 0)
+            return;
+        float a[V], b[V], oa[V], ob[V];
+        widen<T, V>(it.a, a);
+        if (!rotate) {
+            put<T, V>(it.y, a);
             return;
         }
-        if constexpr (INTER) {
-            float o[U];
-#pragma unroll
-            for (int u = 0; u < U; u += 2) {
-                const float2 w = cs[it.pair + u / 2];
-                o[u] = it.a[u] * w.x - it.a[u + 1] * w.y;
-                o[u + 1] = it.a[u + 1] * w.x + it.a[u] * w.y;
-            }
-            if constexpr (V == 1) {
-                float f0[1] = {o[0]}, f1[1] = {o[1]};
-                put<T, 1>(it.y, f0);
-                put<T, 1>(it.y + 1, f1);
-            } else {
-                put<T, V>(it.y, o);
-            }
-        } else {
-            float oa[V], ob[V];
+        const float2 *w = cs + it.t * p.half + pair;
+        if constexpr (kTwo) {
+            widen<T, V>(it.b, b);
 #pragma unroll
             for (int u = 0; u < V; ++u) {
-                const float2 w = cs[it.pair + u];
-                oa[u] = it.a[u] * w.x - it.b[u] * w.y;
-                ob[u] = it.b[u] * w.x + it.a[u] * w.y;
+                oa[u] = a[u] * w[u].x - b[u] * w[u].y;
+                ob[u] = b[u] * w[u].x + a[u] * w[u].y;
             }
             put<T, V>(it.y, oa);
-            put<T, V>(it.y + p.half, ob);
+            put<T, V>(it.y + (INTER ? 1 : p.half), ob);
+        } else {
+#pragma unroll
+            for (int u = 0; u < V; u += 2) {
+                oa[u] = a[u] * w[u / 2].x - a[u + 1] * w[u / 2].y;
+                oa[u + 1] = a[u + 1] * w[u / 2].x + a[u] * w[u / 2].y;
+            }
+            put<T, V>(it.y, oa);
         }
     };
 
-    It it[kRopeHold];
+    bool angles = false;
+    for (int c = c_first; c < p.head_items || !angles; c += p.cols) {
+        const bool on = slot < p.slots && c < p.head_items, rotate = c < p.rot_items;
+        // first element of the item in its head, first pair in the token's angles
+        const int e = rotate ? (INTER && V == 1 ? 2 * c : c * V) : 2 * p.half + (c - p.rot_items) * V;
+        const int pair = INTER ? e / 2 : e;
+        int t = slot / p.heads, h = slot - t * p.heads;
+        auto step = [&] {
+            t += dt;
+            h += dh;
+            if (h >= p.heads) {
+                h -= p.heads;
+                ++t;
+            }
+        };
+        Item it[kRopeHold];
+        bool more = on && t < n_tok;
+        auto fetch_all = [&] {
 #pragma unroll
-    for (int j = 0; j < kRopeHold; ++j)
-        if (tid + j * nt < total)
-            load(tid + j * nt, it[j]);
-    for (int i = tid; i < n_tok * p.half; i += nt) {
-        const int t = i / p.half, j = i - t * p.half;
-        const double at = p.pos64 ? (double)static_cast<const int64_t *>(p.pos)[n0 + t]
-                                  : (double)static_cast<const int32_t *>(p.pos)[n0 + t];
-        // freq / 2 pi is off by 2^-53 of itself, the fma rounds once: at 2^31 positions of
-        // frequency 1 the angle is still within 2^-23
-        const double f = p.freq[j] * 0.15915494309189533577;
-        const double u = fma(at, f, -rint(at * f));
-        float s, c;
-        sincospif(2.f * (float)u, &s, &c);
-        cs[i] = make_float2(c * p.m, s * p.m * p.sign);
-    }
-    __syncthreads();
+            for (int j = 0; j < kRopeHold; ++j) {
+                fetch(it[j], t, h, e, rotate);
+                step();
+            }
+        };
+        if (more)
+            fetch_all();
+        if (!angles) {
+            for (int i = tid; i < n_tok * p.half; i += blockDim.x) {
+                const int tt = i / p.half, j = i - tt * p.half;
+                const double at = p.pos64 ? (double)static_cast<const int64_t *>(p.pos)[n0 + tt]
+                                          : (double)static_cast<const int32_t *>(p.pos)[n0 + tt];
+                // freq / 2 pi is off by 2^-53 of itself, the fma rounds once: at 2^31 positions
+                // of frequency 1 the angle is still within 2^-23
+                const double f = p.freq[j] * 0.15915494309189533577;
+                const double u = fma(at, f, -rint(at * f));
+                float s, co;
+                sincospif(2.f * (float)u, &s, &co);
+                cs[i] = make_float2(co * p.m, s * p.m * p.sign);
+            }
+            __syncthreads();
+            angles = true;
+        }
+        while (more) {
 #pragma unroll
-    for (int j = 0; j < kRopeHold; ++j)
-        if (tid + j * nt < total)
-            store(it[j]);
-    for (int i = tid + kRopeHold * nt; i < total; i += nt) {
-        load(i, it[0]);
-        store(it[0]);
+            for (int j = 0; j < kRopeHold; ++j)
+                finish(it[j], pair, rotate);
+            more = t < n_tok;
+            if (more)
+                fetch_all();
+        }
     }
 }
 
@@ -237,27 +244,22 @@ cudaError_t launch_rope_t(RopeArgs &a, bool vec, bool copy, cudaStream_t s)
     const int rot = 2 * a.half;
     a.rot_items = INTER ? (vec ? rot / VW : a.half) : a.half / V;
     a.head_items = a.rot_items + (copy ? (a.dim - rot) / V : 0);
-    int64_t items = 0;
-    for (int i = 0; i < a.n_mat; ++i) {
-        a.mat[i].first = (int32_t)items;
-        items += (int64_t)a.mat[i].heads * a.head_items;
-    }
-    if (items > (1 << 24))
-        return cudaErrorInvalidValue;
-    a.items = (int32_t)items;
+    a.cols = a.head_items < kRopeThreads ? a.head_items : kRopeThreads;
+    a.slots = kRopeThreads / a.cols;
+    // tokens a block: as many as leave every SM four blocks, up to 8 (their angles cost the
+    // block one wait, and it is spread over all of them), and at least half the threads' worth
+    const int64_t per_tok = (int64_t)a.heads * a.cols;
     a.tokens = 1;
-    while (a.tokens < 8 && a.tokens * items < kRopeThreads / 2)
+    while (a.tokens < 8 && ((int64_t)a.N >= 2 * 4 * 148 * (int64_t)a.tokens || a.tokens * per_tok < kRopeThreads / 2))
         a.tokens *= 2;
-    int threads = kRopeThreads;
-    const int64_t want = (a.tokens * items + kRopeHold - 1) / kRopeHold;
-    while (threads > 64 && threads / 2 >= want)
-        threads /= 2;
+    if (a.slots > (int64_t)a.tokens * a.heads)
+        a.slots = a.tokens * a.heads;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.N + a.tokens - 1) / a.tokens);
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = dim3((a.cols * a.slots + 31) & ~31);
     cfg.dynamicSmemBytes = sizeof(float2) * a.tokens * a.half;
     cfg.stream = s;
     cfg.attrs = attr;
@@ -321,13 +323,10 @@ extern "C" lora_status lora_rope(const lora_rope_mat *mats, int32_t n_mats, int3
         copy |= !same && rot < dim;
         vec &= !((((uintptr_t)m.x | (uintptr_t)m.y) & 15) ||
                  ((m.x_token | m.x_head | m.y_token | m.y_head) & (vw - 1)));
-        a.mat[i] = {m.x, m.y, m.x_token, m.x_head, m.y_token, m.y_head, m.heads, 0};
+        a.mat[i] = {m.x, m.y, m.x_token, m.x_head, m.y_token, m.y_head, a.heads, 0};
+        if (m.heads > LORA_MAX_ROPE_HEADS || (a.heads += m.heads) > LORA_MAX_ROPE_HEADS)
+            return LORA_ERR_UNSUPPORTED;
     }
-    int64_t heads = 0;
-    for (int i = 0; i < n_mats; ++i)
-        heads += mats[i].heads;
-    if (heads > LORA_MAX_ROPE_HEADS)
-        return LORA_ERR_UNSUPPORTED;
     if (N == 0)
         return LORA_OK;
     a.n_mat = n_mats;
