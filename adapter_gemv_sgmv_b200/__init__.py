@@ -390,110 +390,132 @@ def lora_linear_sgmv(X, W, Y, pool, seg_off, seg_ad, scale: float, ws: Workspace
 
 
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
-_dtype_codes: dict = {}                                # torch dtype -> lora_dtype
 
 
-def _dtype(t, name: str) -> int:
-    if not _dtype_codes:
-        torch = _torch()
-        _dtype_codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
-    code = _dtype_codes.get(t.dtype)
+class _T:
+    """What the calls below look up in torch on every call, found once."""
+
+    def __init__(self):
+        import torch
+        self.i8, self.i32, self.i64 = torch.int8, torch.int32, torch.int64
+        self.bf16, self.f32, self.f64 = torch.bfloat16, torch.float32, torch.float64
+        self.codes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}     # lora_dtype
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.current_device = torch._C._cuda_getDevice
+        self.capturing = torch.cuda.is_current_stream_capturing
+        self.device = torch.cuda.device
+        self.stream = torch.cuda.stream
+
+
+_types: _T | None = None
+
+
+def _lib_types():
+    global _types
+    if _types is None:
+        _types = _T()
+    return _lib or load(), _types
+
+
+def _one_device(tensors) -> int:
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            dev = -1
+    if dev < 0:
+        raise LoraError("tensors must live on one CUDA device", 1)
+    return dev
+
+
+def _rows(t, name: str, n: int, d: int):
+    """Leading dimension of a matrix [n, d] (a single row has none: any that fits will do)."""
+    if t.shape != (n, d):
+        raise LoraError(f"{name} must be a tensor [{n}, {d}]", 1)
+    ld, unit = t.stride()
+    if unit != 1 and d > 1:
+        raise LoraError(f"{name} must have unit-stride columns", 1)
+    return ld if n > 1 else (d + 15) // 16 * 16
+
+
+def _code(T, t, name: str) -> int:
+    code = T.codes.get(t.dtype)
     if code is None:
         raise LoraError(f"{name} must be bf16, fp16 or fp32", 2)
     return code
 
 
-def _rows(t, name: str, dtype=None):
-    """Leading dimension of a 2-D tensor of rows (a single row has none: any that fits will do)."""
-    if t.dim() != 2 or (dtype is not None and t.dtype != dtype) or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise LoraError(f"{name} must be a 2-D tensor with unit-stride columns", 1)
-    n, d = t.shape
-    return t.stride(0) if n > 1 else (d + 15) // 16 * 16
-
-
-def _vec(t, n: int, name: str):
-    if t.dtype != _torch().float32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+def _scales(T, t, n: int, name: str):
+    if t.dtype is not T.f32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise LoraError(f"{name} must be a contiguous fp32 tensor of {n} scales", 1)
-
-
-def _device_index(*tensors) -> int:
-    """The one CUDA device the tensors live on."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != dev or not t.is_cuda:
-            raise LoraError("tensors must live on one CUDA device", 1)
-    return dev
-
-
-def _on_device(dev: int, stream, call):
-    """call(raw stream) with `dev` current: a launch goes to the current device, which need
-    not be the tensors'.  Without a stream, that device's current one."""
-    torch = _torch()
-    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
-    if torch._C._cuda_getDevice() == dev:
-        return call(raw)
-    with torch.cuda.device(dev):
-        return call(raw)
 
 
 _stream_ws: dict = {}
 
 
-def _stream_workspace(nbytes: int, dev: int, raw: int, stream) -> Workspace:
+def _stream_workspace(T, nbytes: int, dev: int, raw: int, stream) -> Workspace:
     """A workspace of this device and stream: calls on two streams never share one.  Under graph
     capture it is a fresh one from the graph's memory, so that no two graphs share it."""
-    torch = _torch()
-    if stream is not None and raw != torch._C._cuda_getCurrentRawStream(dev):
-        with torch.cuda.stream(stream):                # allocated, and freed, in that stream's order
-            return _stream_workspace(nbytes, dev, raw, stream)
-    if torch.cuda.is_current_stream_capturing():
-        return Workspace(nbytes, device=torch.device("cuda", dev))
+    if stream is not None and raw != T.raw_stream(dev):
+        with T.stream(stream):                         # allocated, and freed, in that stream's order
+            return _stream_workspace(T, nbytes, dev, raw, None)
+    if T.capturing():
+        return Workspace(nbytes, device=f"cuda:{dev}")
     ws = _stream_ws.get((dev, raw))
     if ws is None or ws.nbytes < nbytes:
-        ws = _stream_ws[dev, raw] = Workspace(max(nbytes, 2 * (ws.nbytes if ws else 0)),
-                                              device=torch.device("cuda", dev))
+        ws = _stream_ws[dev, raw] = Workspace(max(nbytes, 2 * (ws.nbytes if ws else 0)), device=f"cuda:{dev}")
     return ws
 
 
+# Each call below launches on the tensors' device: where that is not the current one, it runs
+# again with that device current.
+
 def lora_quant_i8(X, Q, S, stream=None):
     """Q[n] = round(127 X[n] / max|X[n]|) (int8), S[n] = max|X[n]| / 127 for rows of bf16, fp16 or fp32."""
-    lib = load()
-    dev = _device_index(X, Q, S)
-    ldx, ldq = _rows(X, "X"), _rows(Q, "Q", _torch().int8)
-    if Q.shape != X.shape:
-        raise LoraError("Q must have X's shape", 1)
+    lib, T = _lib_types()
+    dev = _one_device((X, Q, S))
+    if T.current_device() != dev:
+        with T.device(dev):
+            return lora_quant_i8(X, Q, S, stream)
+    if X.dim() != 2:
+        raise LoraError("X must be a 2-D tensor", 1)
     n, d = X.shape
-    _vec(S, n, "S")
-    dt = _dtype(X, "X")
-    _rc(_on_device(dev, stream, lambda raw: lib.lora_quant_i8(
-        X.data_ptr(), dt, ldx, Q.data_ptr(), ldq, S.data_ptr(), n, d, raw)), "lora_quant_i8")
+    ldx, ldq = _rows(X, "X", n, d), _rows(Q, "Q", n, d)
+    if Q.dtype is not T.i8:
+        raise LoraError("Q must be int8", 1)
+    _scales(T, S, n, "S")
+    rc = lib.lora_quant_i8(X.data_ptr(), _code(T, X, "X"), ldx, Q.data_ptr(), ldq, S.data_ptr(), n, d,
+                           T.raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        raise LoraError("lora_quant_i8", rc)
 
 
-def _i8_operands(Q, Sx, Wq, Sw, Y):
-    i8 = _torch().int8
-    ldq, ldw, ldy = _rows(Q, "Q", i8), _rows(Wq, "Wq", i8), _rows(Y, "Y")
-    (n, d_in), d_out = Q.shape, Wq.shape[0]
-    if Wq.shape[1] != d_in or Y.shape[0] != n or Y.shape[1] != d_out:
-        raise LoraError("Q [N, d_in], Wq [d_out, d_in] and Y [N, d_out] do not fit together", 1)
-    _vec(Sx, n, "Sx")
-    _vec(Sw, d_out, "Sw")
-    return ldq, ldw, ldy, n, d_in, d_out
+def _i8_operands(T, Q, Sx, Wq, Sw, Y):
+    if Q.dtype is not T.i8 or Wq.dtype is not T.i8 or Q.dim() != 2 or Wq.dim() != 2:
+        raise LoraError("Q [N, d_in] and Wq [d_out, d_in] must be int8 matrices", 1)
+    n, d_in = Q.shape
+    d_out = Wq.shape[0]
+    _scales(T, Sx, n, "Sx")
+    _scales(T, Sw, d_out, "Sw")
+    return n, d_in, d_out, _rows(Q, "Q", n, d_in), _rows(Wq, "Wq", d_out, d_in), _rows(Y, "Y", n, d_out)
 
 
 def lora_linear_i8(Q, Sx, Wq, Sw, Y, ws: Workspace | None = None, stream=None):
     """Y[n][o] = Sx[n] Sw[o] sum_i Q[n][i] Wq[o][i] for int8 tokens and weight; Y is bf16, fp16 or
     fp32 and overwritten.  Returns the workspace (its error word: lora_get_error)."""
-    lib = load()
-    dev = _device_index(Q, Sx, Wq, Sw, Y)
-    ldq, ldw, ldy, n, d_in, d_out = _i8_operands(Q, Sx, Wq, Sw, Y)
-    dt = _dtype(Y, "Y")
-
-    def call(raw):
-        w = ws or _stream_workspace(256, dev, raw, stream)
-        _rc(lib.lora_linear_i8(Q.data_ptr(), ldq, Sx.data_ptr(), Wq.data_ptr(), ldw, Sw.data_ptr(), Y.data_ptr(), dt,
-                               ldy, n, d_in, d_out, w.ptr(), w.nbytes, raw), "lora_linear_i8")
-        return w
-    return _on_device(dev, stream, call)
+    lib, T = _lib_types()
+    dev = _one_device((Q, Sx, Wq, Sw, Y))
+    if T.current_device() != dev:
+        with T.device(dev):
+            return lora_linear_i8(Q, Sx, Wq, Sw, Y, ws, stream)
+    n, d_in, d_out, ldq, ldw, ldy = _i8_operands(T, Q, Sx, Wq, Sw, Y)
+    raw = T.raw_stream(dev) if stream is None else stream.cuda_stream
+    if ws is None:
+        ws = _stream_workspace(T, 256, dev, raw, stream)
+    rc = lib.lora_linear_i8(Q.data_ptr(), ldq, Sx.data_ptr(), Wq.data_ptr(), ldw, Sw.data_ptr(), Y.data_ptr(),
+                            _code(T, Y, "Y"), ldy, n, d_in, d_out, ws.ptr(), ws.nbytes, raw)
+    if rc:
+        raise LoraError("lora_linear_i8", rc)
+    return ws
 
 
 def lora_linear_i8_sgmv(Q, Sx, X, Wq, Sw, Y, pool, seg_off, seg_ad, scale: float, ws: Workspace | None = None,
@@ -502,30 +524,32 @@ def lora_linear_i8_sgmv(Q, Sx, X, Wq, Sw, Y, pool, seg_off, seg_ad, scale: float
 
     X holds the bf16 tokens that Q and Sx are the 8-bit form of; Y is bf16, overwritten inside
     the segments and left alone outside them."""
-    lib = load()
-    torch = _torch()
-    dev = _device_index(Q, Sx, X, Wq, Sw, Y, seg_off, seg_ad, pool.A, pool.B, pool.A_off, pool.B_off, pool.rank)
-    ldq, ldw, ldy, n, d_in, d_out = _i8_operands(Q, Sx, Wq, Sw, Y)
+    lib, T = _lib_types()
+    dev = _one_device((Q, Sx, X, Wq, Sw, Y, seg_off, seg_ad, pool.A, pool.B, pool.A_off, pool.B_off, pool.rank))
+    if T.current_device() != dev:
+        with T.device(dev):
+            return lora_linear_i8_sgmv(Q, Sx, X, Wq, Sw, Y, pool, seg_off, seg_ad, scale, ws, stream, max_rank)
+    n, d_in, d_out, ldq, ldw, ldy = _i8_operands(T, Q, Sx, Wq, Sw, Y)
     ps = make_pool_struct(pool, max_rank)
-    ldx = _rows(X, "X", torch.bfloat16)
-    if Y.dtype != torch.bfloat16:
-        raise LoraError("Y must be bf16", 1)
-    if d_in != ps.d_in or d_out != ps.d_out or X.shape != Q.shape:
-        raise LoraError("Q, X, Wq and the pool disagree on N, d_in or d_out", 1)
+    ldx = _rows(X, "X", n, d_in)
+    if X.dtype is not T.bf16 or Y.dtype is not T.bf16:
+        raise LoraError("X and Y must be bf16", 1)
+    if d_in != ps.d_in or d_out != ps.d_out:
+        raise LoraError("Wq must be [pool.d_out, pool.d_in]", 1)
     n_seg = seg_ad.numel()
     for t, need, name in ((seg_off, n_seg + 1, "seg_off"), (seg_ad, n_seg, "seg_ad")):
-        if t.dtype != torch.int32 or t.numel() < need or not t.is_contiguous():
+        if t.dtype is not T.i32 or t.numel() < need or not t.is_contiguous():
             raise LoraError(f"{name} must be a contiguous int32 tensor of {need} entries", 1)
-
-    def call(raw):
-        w = ws or _stream_workspace(lora_workspace_size(OP_LINEAR_I8_SGMV, n, ps.n_adapters, d_in, d_out, ps.max_rank,
-                                                        n_seg), dev, raw, stream)
-        _rc(lib.lora_linear_i8_sgmv(Q.data_ptr(), ldq, Sx.data_ptr(), X.data_ptr(), ldx, Wq.data_ptr(), ldw,
-                                    Sw.data_ptr(), Y.data_ptr(), ldy, ctypes.byref(ps), seg_off.data_ptr(),
-                                    seg_ad.data_ptr(), n_seg, n, float(scale), w.ptr(), w.nbytes, raw),
-            "lora_linear_i8_sgmv")
-        return w
-    return _on_device(dev, stream, call)
+    raw = T.raw_stream(dev) if stream is None else stream.cuda_stream
+    if ws is None:
+        need = lib.lora_workspace_size(OP_LINEAR_I8_SGMV, n, ps.n_adapters, d_in, d_out, ps.max_rank, n_seg, 1)
+        ws = _stream_workspace(T, need, dev, raw, stream)
+    rc = lib.lora_linear_i8_sgmv(Q.data_ptr(), ldq, Sx.data_ptr(), X.data_ptr(), ldx, Wq.data_ptr(), ldw,
+                                 Sw.data_ptr(), Y.data_ptr(), ldy, ctypes.byref(ps), seg_off.data_ptr(),
+                                 seg_ad.data_ptr(), n_seg, n, scale, ws.ptr(), ws.nbytes, raw)
+    if rc:
+        raise LoraError("lora_linear_i8_sgmv", rc)
+    return ws
 
 
 def lora_rope(xs, ys, pos, freqs, interleaved: bool = False, mscale: float = 1.0, inverse: bool = False,
@@ -534,35 +558,39 @@ def lora_rope(xs, ys, pos, freqs, interleaved: bool = False, mscale: float = 1.0
 
     ys[i] receives xs[i] rotated by pos * freqs (ys[i] may be xs[i] itself: in place).  freqs: fp64
     [rot / 2] on the device, rot <= dim; pos: int32 or int64 [N].  `inverse` turns back: the gradient."""
-    lib = load()
-    torch = _torch()
+    lib, T = _lib_types()
     k = len(xs)
     if k == 0 or k != len(ys):
         raise LoraError("one output per input", 1)
-    dev = _device_index(pos, freqs, *xs, *ys)
+    dev = _one_device((pos, freqs, *xs, *ys))
+    if T.current_device() != dev:
+        with T.device(dev):
+            return lora_rope(xs, ys, pos, freqs, interleaved, mscale, inverse, stream)
     x0 = xs[0]
     if x0.dim() != 3:
         raise LoraError("tensors must be [N, heads, dim]", 1)
     n, _, dim = x0.shape
-    mats = (LoraRopeMat * k)()
-    for m, x, y in zip(mats, xs, ys):
-        if (x.dim() != 3 or x.shape != y.shape or x.dtype != x0.dtype or y.dtype != x0.dtype or x.shape[0] != n or
-                x.shape[2] != dim):
+    dt = x0.dtype
+    args = []
+    for x, y in zip(xs, ys):
+        shape = x.shape
+        if len(shape) != 3 or shape[0] != n or shape[2] != dim or y.shape != shape or x.dtype is not dt or \
+                y.dtype is not dt:
             raise LoraError("tensors [N, heads, dim] of one type, N and dim", 1)
-        m.x_token, m.x_head, sx = x.stride()
-        m.y_token, m.y_head, sy = y.stride()
-        if sx != 1 or sy != 1:
+        xt, xh, xu = x.stride()
+        yt, yh, yu = y.stride()
+        if xu != 1 or yu != 1:
             raise LoraError("unit stride inside a head", 1)
-        m.x, m.y, m.heads = x.data_ptr(), y.data_ptr(), x.shape[1]
-    if pos.dtype not in (torch.int32, torch.int64) or pos.dim() != 1 or pos.shape[0] != n or (
-            n > 1 and pos.stride(0) != 1):
+        args.append((x.data_ptr(), y.data_ptr(), xt, xh, yt, yh, shape[1]))
+    if (pos.dtype is not T.i64 and pos.dtype is not T.i32) or pos.shape != (n,) or (n > 1 and pos.stride(0) != 1):
         raise LoraError("pos must be a contiguous int32 or int64 tensor [N]", 1)
-    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+    if freqs.dtype is not T.f64 or freqs.dim() != 1 or not freqs.is_contiguous():
         raise LoraError("freqs must be a contiguous fp64 tensor [rot / 2]", 1)
-    dt = _dtype(x0, "x")
-    _rc(_on_device(dev, stream, lambda raw: lib.lora_rope(
-        mats, k, dt, pos.data_ptr(), pos.element_size(), freqs.data_ptr(), n, dim, 2 * freqs.shape[0],
-        1 if interleaved else 0, 1 if inverse else 0, mscale, raw)), "lora_rope")
+    rc = lib.lora_rope((LoraRopeMat * k)(*args), k, _code(T, x0, "x"), pos.data_ptr(), 8 if pos.dtype is T.i64 else 4,
+                       freqs.data_ptr(), n, dim, 2 * freqs.shape[0], 1 if interleaved else 0, 1 if inverse else 0,
+                       mscale, T.raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        raise LoraError("lora_rope", rc)
 
 
 def lora_rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, low: float = 1.0,

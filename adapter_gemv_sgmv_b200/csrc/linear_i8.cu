@@ -96,6 +96,15 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b
         : "memory");
 }
 
+__device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
 // Arrive on the barrier at this offset in both CTAs when the MMAs issued so far complete.
 __device__ __forceinline__ void commit_pair(uint64_t *bar)
 {
@@ -672,6 +681,204 @@ done:
     }
 }
 
+// ------------------------------------------------------------------ few tokens
+// k_i8_few, decode batches: the weight is what has to be read, so it takes the rows of the
+// MMA (M = 128 output channels) and the tokens its columns (N = 16 .. 256).  The reduction
+// is split over the CTAs of a cluster, which puts every SM to work on one weight; each CTA
+// leaves its 32-bit partial sums in its shared memory and finishes a share of the tokens by
+// reading the other CTAs' (integers: the order of the sum does not matter).  Weights do not
+// come from the kernel before (which quantises the tokens), so their lines are requested
+// into L2 ahead of the wait for it -- a prefetch only: the loads follow the wait, for that
+// kernel may have written this very weight.
+constexpr int kFewThreads = 192;         // producer, MMA issuer, 4 warps that empty the accumulator
+
+template <int NT> struct FewCfg {
+    static constexpr int stage = kAtom + NT * 128;
+    // two CTAs to an SM up to 128 tokens
+    static constexpr int stages = NT <= 32 ? 5 : (NT <= 64 ? 4 : (NT <= 128 ? 3 : 4));
+    static constexpr int smem = stages * stage + 1024;
+    static_assert(NT * 512 <= stages * stage, "the partial sums take the ring's place");
+};
+
+struct FewTc {
+    I8Args a;
+    CUtensorMap map_q;       // tokens, boxes 128 bytes x NT rows
+    CUtensorMap map_w;       // weight, boxes 128 bytes x 128 rows
+    int32_t split;           // CTAs of a cluster
+    unsigned long long wait_ns;
+    int32_t test_stall;
+};
+
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap *map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+
+__device__ __forceinline__ int4 ld_remote_v4(uint32_t addr)
+{
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ int ld_remote(uint32_t addr)
+{
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+template <int NT, class T>
+__global__ void __launch_bounds__(kFewThreads) k_i8_few(const __grid_constant__ FewTc p)
+{
+    using C = FewCfg<NT>;
+    constexpr int kStages = C::stages, kCols = NT < 32 ? 32 : NT;
+    extern __shared__ __align__(1024) unsigned char sm_dyn[];
+    // (every CTA of the cluster has its ring at the same offset: the launch gives all one base)
+    unsigned char *sm = sm_dyn + ((1024 - (smem_u32(sm_dyn) & 1023)) & 1023);
+    __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], acc_full, mma_drain;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int split = p.split, rank = (int)cluster_rank();
+    const int o0 = (blockIdx.x / split) * 128, n0 = blockIdx.y * NT;
+    const int nv = min(NT, p.a.N - n0);
+    const int n_kb = (p.a.d_in + kKB - 1) / kKB;
+    const int k0 = rank * n_kb / split, k1 = (rank + 1) * n_kb / split;
+    int issued = 0;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full_bar[s], 1);
+            mbar_init(&empty_bar[s], 1);
+        }
+        mbar_init(&acc_full, 1);
+        mbar_init(&mma_drain, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        for (int k = k0; k < k1; ++k)
+            tma_prefetch(&p.map_w, k * kKB, o0);
+    }
+    if (warp == 1)
+        tmem_alloc(&tmem_base, kCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    pdl_wait();
+    pdl_trigger();
+
+    if (warp == 0) {
+        if (lane == 0 && !p.test_stall) {
+            const uint64_t pol_x = policy_evict_last(), pol_w = policy_evict_first();
+            for (int k = k0; k < k1; ++k, ++issued) {
+                const int s = issued % kStages;
+                if (!mbar_wait(&empty_bar[s], ((issued / kStages) & 1) ^ 1, &abort_flag, p.a.err, p.wait_ns))
+                    break;
+                mbar_arrive_expect_tx(&full_bar[s], C::stage);
+                tma_load_2d_hint(sm + s * C::stage, &p.map_w, &full_bar[s], k * kKB, o0, pol_w);
+                tma_load_2d_hint(sm + s * C::stage + kAtom, &p.map_q, &full_bar[s], k * kKB, n0, pol_x);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_i8(128, NT);
+            const uint64_t a0 = sw128_desc(smem_u32(sm)), b0 = sw128_desc(smem_u32(sm) + kAtom);
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int k = k0; k < k1; ++k) {
+                if (!(ok = mbar_wait(&full_bar[s], ph, &abort_flag, p.a.err, p.wait_ns)))
+                    break;
+                tc_fence_after();
+                const uint64_t at = (uint64_t)(s * (C::stage >> 4));
+#pragma unroll
+                for (int i = 0; i < kKB / 32; ++i)
+                    mma_i8(tmem, a0 + at + i * 2, b0 + at + i * 2, idesc, (k > k0 || i > 0) ? 1u : 0u);
+                tc_commit(&empty_bar[s]);
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+            if (ok)
+                tc_commit(&acc_full);
+        }
+    } else {
+        // partial sums to shared memory as [token][128 outputs], in the ring's place: every
+        // fill has been multiplied when the accumulator is full
+        const int q = warp & 3;
+        if (warp_wait(&acc_full, 0, &abort_flag, p.a.err, p.wait_ns)) {
+            tc_fence_after();
+            int *part = reinterpret_cast<int *>(sm) + q * 32 + lane;
+#pragma unroll 1
+            for (int c = 0; c < nv; c += 16) {
+                uint32_t w[16];
+                tmem_ld16_raw(tmem + ((uint32_t)(q * 32) << 16) + c, w);
+                tmem_wait(w);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    part[(c + i) * 128] = (int)w[i];
+            }
+            tc_fence_before();
+        }
+    }
+    __syncwarp();
+    if (warp == 0 && lane == 0)
+        drain_fills(full_bar, kStages, issued, p.a.err, p.wait_ns);
+    if (warp == 1 && lane == 0)
+        drain_mma(&mma_drain, 0, p.a.err, p.wait_ns);
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kCols);
+    }
+    __syncwarp();
+    cluster_sync();
+    // a CTA that gave up has no sums to offer: then no output of the tile is written
+    bool whole = true;
+    for (int r = 0; r < split; ++r)
+        whole &= ld_remote(map_rank(smem_u32(&abort_flag), r)) == 0;
+    const int per = (nv + split - 1) / split;
+    const int o = o0 + lane * 4;
+    if (whole && o < p.a.d_out) {
+        const uint32_t mine = smem_u32(sm) + lane * 16;
+        float sw[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            sw[i] = __ldg(p.a.Sw + o + i);
+        for (int t = rank * per + warp; t < min(nv, (rank + 1) * per); t += kFewThreads / 32) {
+            int4 v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < split)
+                    v[r] = ld_remote_v4(map_rank(mine + t * 512, r));
+            const float sx = __ldg(p.a.Sx + n0 + t);
+            int4 a = v[0];
+#pragma unroll
+            for (int r = 1; r < 8; ++r)
+                if (r < split) {
+                    a.x += v[r].x;
+                    a.y += v[r].y;
+                    a.z += v[r].z;
+                    a.w += v[r].w;
+                }
+            const float y0 = (float)a.x * (sx * sw[0]), y1 = (float)a.y * (sx * sw[1]);
+            const float y2 = (float)a.z * (sx * sw[2]), y3 = (float)a.w * (sx * sw[3]);
+            T *y = static_cast<T *>(p.a.Y) + (int64_t)(n0 + t) * p.a.ldy + o;
+            if constexpr (sizeof(T) == 4)
+                *reinterpret_cast<float4 *>(y) = make_float4(y0, y1, y2, y3);
+            else
+                *reinterpret_cast<uint2 *>(y) = make_uint2(pack2(y0, y1, T()), pack2(y2, y3, T()));
+        }
+    }
+    __syncwarp();
+    cluster_sync();                                  // (its sums are read: a CTA may go)
+}
+
 bool encode_y(CUtensorMap *m, void *Y, int32_t dtype, int64_t rows, int64_t cols, int64_t ld)
 {
     EncodeTiledFn fn = encode_fn();
@@ -751,15 +958,116 @@ template <bool LORA, class T> cudaError_t launch_pair(const I8Args &a, int64_t m
     return cudaLaunchKernelEx(&cfg, k_i8_pair<LORA, T>, p);
 }
 
+template <int NT, class T> cudaError_t launch_few(const I8Args &a, int split, cudaStream_t s, bool *ok)
+{
+    using C = FewCfg<NT>;
+    FewTc p = {};
+    p.a = a;
+    p.split = split;
+    *ok = encode_box8(&p.map_q, a.Q, a.N, a.d_in, a.ldq, NT) && encode_box8(&p.map_w, a.W, a.d_out, a.d_in, a.ldw, 128);
+    if (!*ok)
+        return cudaSuccess;
+    p.wait_ns = wait_bound_ns();
+    p.test_stall = test_stall_mode();
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        if ((e = cudaFuncSetAttribute(k_i8_few<NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem)) != cudaSuccess)
+            return e;
+        if (dev >= 0 && dev < 64)
+            attr_set[dev] = true;
+    }
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.d_out + 127) / 128 * split, (a.N + NT - 1) / NT);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = C::smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_i8_few<NT, T>, p);
+}
+
+// Microseconds of a call without adapters, by a model fitted to B200 timings over N = 1 ..
+// 2048 and weights of 4096 x 1024 to 4096 x 14336 and 14336 x 4096, weights from HBM:
+// * CTA pairs: 6 and 0.29 per k-block of every round of tiles over the 74 pairs of SMs;
+// * few tokens: the ring's traffic at 85 bytes a nanosecond and SM, and 5.5 to 8 for launch,
+//   first loads, the exchange of partial sums and the last stores.
+// Measured on both sides (us, pairs / few): 1 x 4096 -> 4096 15.5 / 6.4; 256 x 4096 -> 4096
+// 16.3 / 12.4; 256 x 4096 -> 14336 18.5 / 28; 512 x 4096 -> 4096 16.7 / 16.1; 1024 x 4096 ->
+// 1024 16.0 / 11.9; 1024 x 4096 -> 4096 17.5 / 26.
+double pair_us(const I8Args &a, int n_kb)
+{
+    const int64_t tiles = ((int64_t)a.N + 255) / 256 * ((a.d_out + 255) / 256);
+    return 6.0 + (double)((tiles + 73) / 74) * n_kb * 0.29;
+}
+
+double few_us(const I8Args &a, int n_kb, int nt, int split)
+{
+    const int64_t ctas = (int64_t)((a.d_out + 127) / 128) * (((int64_t)a.N + nt - 1) / nt) * split;
+    const int64_t slots = nt <= 128 ? 296 : 148;
+    double load = (double)ctas / 148;                // CTAs an SM works through
+    if (load < 1)
+        load = 1;
+    if (ctas > slots)
+        load = (double)((ctas + slots - 1) / slots * slots) / 148;
+    const int kb = (n_kb + split - 1) / split;
+    return (nt <= 64 ? 5.5 : (nt <= 128 ? 6.5 : 8.1)) + load * kb * (16384 + nt * 128) / 85e3;
+}
+
+template <class T> cudaError_t launch_any(const I8Args &a, cudaStream_t s, bool *ok)
+{
+    const int n_kb = (a.d_in + kKB - 1) / kKB;
+    double best = pair_us(a, n_kb);
+    int best_nt = 0, best_split = 1;
+    for (int nt : {16, 32, 64, 128, 256}) {
+        if (nt < 128 && nt < a.N)                    // narrow tiles would read the weight again and again
+            continue;
+        for (int split = 1; split <= 8 && (split == 1 || 2 * split <= n_kb); split *= 2) {
+            const double us = few_us(a, n_kb, nt, split);
+            if (us < best) {
+                best = us;
+                best_nt = nt;
+                best_split = split;
+            }
+        }
+        if (nt >= a.N)
+            break;
+    }
+    switch (best_nt) {
+    case 16:
+        return launch_few<16, T>(a, best_split, s, ok);
+    case 32:
+        return launch_few<32, T>(a, best_split, s, ok);
+    case 64:
+        return launch_few<64, T>(a, best_split, s, ok);
+    case 128:
+        return launch_few<128, T>(a, best_split, s, ok);
+    case 256:
+        return launch_few<256, T>(a, best_split, s, ok);
+    default:
+        return launch_pair<false, T>(a, 0, s, ok);
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_linear_i8(const I8Args &a, int max_tiles, cudaStream_t s, bool *ok)
 {
     if (a.groups)
         return launch_pair<true, __nv_bfloat16>(a, max_tiles, s, ok);
-    return a.dtype == LORA_BF16 ? launch_pair<false, __nv_bfloat16>(a, 0, s, ok)
-         : a.dtype == LORA_F16 ? launch_pair<false, __half>(a, 0, s, ok)
-                               : launch_pair<false, float>(a, 0, s, ok);
+    return a.dtype == LORA_BF16 ? launch_any<__nv_bfloat16>(a, s, ok)
+         : a.dtype == LORA_F16 ? launch_any<__half>(a, s, ok)
+                               : launch_any<float>(a, s, ok);
 }
 
 }  // namespace lora

@@ -403,3 +403,48 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for job in jobs:
         check_parity(widen(to_host(job[5])), job[8], "two streams")
+
+
+# ------------------------------------------------------------------ waits run out
+def _stalled(fn):
+    """Run fn() with the testing hook on: no loads are issued and waits end after 20 us."""
+    L.lora_test_stall(True, 20e-6)
+    try:
+        ws = fn()
+        torch.cuda.synchronize()
+    finally:
+        L.lora_test_stall(False)
+    return L.lora_get_error(ws)
+
+
+@pytest.mark.parametrize("N", [1, 40, 200, 2600])
+def test_linear_times_out_and_recovers(N):
+    """Both kernels (few tokens, CTA pairs): the status bit, y untouched, and the next call right."""
+    d_in, d_out = 1024, 1032
+    q = torch.randint(-127, 128, (N, d_in), dtype=torch.int8, device=DEV)
+    w = torch.randint(-127, 128, (d_out, d_in), dtype=torch.int8, device=DEV)
+    Sx, Sw = torch.ones(N, device=DEV), torch.ones(d_out, device=DEV)
+    Y = torch.full((N, d_out), 5.0, device=DEV)
+    assert _stalled(lambda: L.lora_linear_i8(q, Sx, w, Sw, Y)) & 64
+    assert torch.all(Y == 5)
+    ws = L.lora_linear_i8(q, Sx, w, Sw, Y)
+    assert L.lora_get_error(ws) == 0
+    # (sums reach 2^24: their conversion to fp32 rounds)
+    want = q.double() @ w.double().t()
+    assert float(((Y.double() - want).abs() - want.abs() * 2.0 ** -24).max()) <= 0
+
+
+def test_adapted_times_out_and_recovers():
+    rng = np.random.default_rng(45)
+    d_in, d_out = 256, 520
+    hp = rand_host_pool(rng, [32, 64], d_in, d_out)
+    off, ads, N = np.array([0, 300, 700], np.int32), np.array([1, 0], np.int32), 700
+    X, x, Q, Sx, Wq, Sw, base = _adapted_inputs(rng, N, d_in, d_out)
+    pool = DevPool(hp)
+    Y = torch.ones((N, d_out), dtype=torch.bfloat16, device=DEV)
+    assert _stalled(lambda: L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, pool, _i32(off), _i32(ads), 0.5)) & 64
+    assert torch.all(Y == 1)
+    ws = L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, pool, _i32(off), _i32(ads), 0.5)
+    assert L.lora_get_error(ws) == 0
+    want = base + oracle.linear_sgmv(X, np.zeros((d_out, d_in), np.uint16), hp, off, ads, 0.5)
+    check_parity(widen(to_host(Y)), want, "adapted after a timeout")
