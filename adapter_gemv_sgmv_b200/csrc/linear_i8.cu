@@ -35,8 +35,6 @@
 namespace lora {
 namespace {
 
-constexpr int kPThreads = 320;
-constexpr int kPEpiWarps = 8;
 constexpr int kPNsBlock = 8;            // output slices per block of the tile order
 constexpr int kKB = 128;                // bytes of the reduction per k-block
 
@@ -123,10 +121,11 @@ __host__ __device__ constexpr uint32_t idesc_i8(int M, int N)
 // ------------------------------------------------------------------ the tiles
 template <bool LORA> struct PairCfg;
 template <> struct PairCfg<false> {
-    static constexpr int BN = 256, stages = 6, buffers = 2;
+    static constexpr int BN = 256, stages = 6, buffers = 2, epi_warps = 8, box_cols = 128;   // (bytes)
 };
 template <> struct PairCfg<true> {
-    static constexpr int BN = 256, stages = 5, buffers = 1;
+    // (twice the epilogue warps: nothing runs under them)
+    static constexpr int BN = 256, stages = 5, buffers = 1, epi_warps = 16, box_cols = 64;
 };
 
 struct PairTc {
@@ -160,89 +159,109 @@ __device__ __forceinline__ PairTile pair_tile(int64_t u, int n_pairs, int n_ns)
     return t;
 }
 
-struct PairAd {
-    int r;          // rank, 0: no delta
-    int m;          // B view, -1: rows gathered
-    int64_t boff;
+// ------------------------------------------------------------- segments (LORA)
+// A tile is 256 consecutive rows, whatever segments they belong to: the base product does
+// not ask.  The delta does: the tile's runs of rows with one adapter make one pass each,
+// and a row is taken from the pass of its own adapter (rows without one from the first).
+// The segments' bounds and adapters are looked up once, by all threads, when the CTA
+// starts: four dependent loads from global memory each, which every role would otherwise
+// wait for in every tile.
+struct __align__(16) SegAd {
+    int64_t boff;    // the adapter's B
+    int32_t a;       // adapter
+    int16_t r;       // rank, 0: no delta
+    int16_t m;       // B view, -1: rows gathered
+};
+constexpr int kSegTable = 512;          // segments in shared memory; more are looked up as they come
+
+struct SegTable {
+    SegAd ad[kSegTable];
+    int32_t off[kSegTable + 1];
 };
 
-// The row tiles of a pair and the delta's passes: pass 0 takes the first tile's adapter
-// (and the second's, if it is the same), pass 1 the second's.  Packed, as it lies in
-// shared memory: finding it takes five dependent loads from global memory (tile, segment,
-// adapter, its metadata), more than a microsecond that every role of every tile would
-// wait for, so the CTA's threads look up all of its tiles at once when it starts.
-struct __align__(16) PairRows {
-    int64_t boff[2];
-    int32_t row[2];
-    uint16_t cnt[2];
-    uint16_t ad[2];      // rank | (view index + 1) << 8 | same adapter as tile 0 << 15
+__device__ SegAd seg_lookup(const PairTc &p, int k, bool report)
+{
+    SegAd x = {0, -1, 0, -1};
+    const int32_t a = p.a.seg_ad[k];
+    int32_t r = 0;
+    int64_t ao = 0, bo = 0;
+    if (a == -1)
+        return x;
+    if (!pool_adapter_ok(p.a.pool, a, &r, &ao, &bo)) {
+        if (report)
+            atomicOr(p.a.err, (uint32_t)LORA_ERR_BAD_ADAPTER);
+        return x;
+    }
+    // (the view's row index of the last box has to fit 32 bits)
+    int m = b_map(r);
+    if (m >= 0 && (!((p.b_tma >> m) & 1) || bo % r != 0 || bo / r + p.a.d_out + 512 > 0x7fffffffLL))
+        m = -1;
+    x.boff = bo;
+    x.a = a;
+    x.r = (int16_t)r;
+    x.m = (int16_t)m;
+    return x;
+}
 
-    __device__ PairAd adapter(int t) const
+struct Segments {
+    const PairTc &p;
+    const SegTable *tab;
+    bool in_tab;
+
+    __device__ int start(int k) const { return in_tab ? tab->off[k] : p.a.seg_off[k]; }
+    __device__ SegAd ad(int k) const { return in_tab ? tab->ad[k] : seg_lookup(p, k, false); }
+    // the segment of a row (start(0) <= row < start(n_seg)): the last one that starts at or before it
+    __device__ int of_row(int row) const
     {
-        PairAd d;
-        d.r = ad[t] & 0xff;
-        d.m = ((ad[t] >> 8) & 7) - 1;
-        d.boff = boff[t];
-        return d;
-    }
-    __device__ bool same() const { return ad[1] >> 15; }
-    // bf16 k-blocks of a pass: high and low parts of every 64 rank columns
-    __device__ int nf(int pass) const { return pass && same() ? 0 : 2 * (((ad[pass] & 0xff) + 63) >> 6); }
-};
-constexpr int kPTable = 256;            // tiles of a CTA looked up when it starts
-
-__device__ PairRows pair_lookup(const PairTc &p, int pair, int n_tiles, bool report)
-{
-    PairRows x;
-    int32_t a[2] = {-1, -1};
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        x.row[t] = p.a.N;                            // no tile: boxes past the end, zeros
-        x.cnt[t] = 0;
-        x.ad[t] = 0;
-        x.boff[t] = 0;
-        if (2 * pair + t >= n_tiles)
-            continue;
-        const Group g = p.a.groups[2 * pair + t];
-        x.row[t] = g.p0;
-        x.cnt[t] = (uint16_t)g.cnt;
-        a[t] = p.a.seg_ad[g.item];
-        int32_t r = 0;
-        int64_t ao = 0, bo = 0;
-        if (a[t] == -1)
-            continue;
-        if (!pool_adapter_ok(p.a.pool, a[t], &r, &ao, &bo)) {
-            if (report)
-                atomicOr(p.a.err, (uint32_t)LORA_ERR_BAD_ADAPTER);
-            a[t] = -1;
-            continue;
+        int lo = 0, hi = p.a.n_seg;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (start(mid) <= row)
+                lo = mid;
+            else
+                hi = mid;
         }
-        // (the view's row index of the last box has to fit 32 bits)
-        int m = b_map(r);
-        if (m >= 0 && (!((p.b_tma >> m) & 1) || bo % r != 0 || bo / r + p.a.d_out + 512 > 0x7fffffffLL))
-            m = -1;
-        x.boff[t] = bo;
-        x.ad[t] = (uint16_t)(r | (m + 1) << 8 | (t && a[0] == a[1] ? 0x8000 : 0));
+        return lo;
     }
-    return x;
-}
+};
 
-template <bool LORA>
-__device__ __forceinline__ PairRows pair_rows(const PairTc &p, const PairRows *tab, int i, int pair, int n_tiles)
-{
-    if constexpr (LORA) {
-        if (i < kPTable)
-            return tab[i];
-        return pair_lookup(p, pair, n_tiles, false);
+// The runs of rows with one adapter in a tile, in order.
+struct Runs {
+    const Segments &sg;
+    int k, end;          // next segment; the tile's end
+    int r0, r1;          // the run
+    SegAd ad;
+
+    __device__ Runs(const Segments &sg_, int row0, int end_) : sg(sg_), k(sg_.of_row(row0)), end(end_), r0(0), r1(0)
+    {
+        ad.r = 0;
     }
-    PairRows x = {};
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        x.row[t] = pair * 256 + t * 128;
-        x.cnt[t] = (uint16_t)max(0, min(128, p.a.N - x.row[t]));
+    __device__ bool next()
+    {
+        for (; k < sg.p.a.n_seg; ++k) {
+            r0 = sg.start(k);
+            if (r0 >= end)
+                break;
+            r1 = sg.start(k + 1);
+            if (r1 == r0)
+                continue;
+            ad = sg.ad(k);
+            if (ad.r == 0)
+                continue;
+            for (++k; k < sg.p.a.n_seg && r1 < end; ++k) {           // more of the same adapter
+                const int e = sg.start(k + 1);
+                if (e != r1 && sg.ad(k).a != ad.a)
+                    break;
+                r1 = e;
+            }
+            return true;
+        }
+        ad.r = 0;
+        return false;
     }
-    return x;
-}
+    // bf16 k-blocks: high and low parts of every 64 rank columns
+    __device__ int kblocks() const { return 2 * ((ad.r + 63) >> 6); }
+};
 
 __device__ __forceinline__ void tmem_ld16_raw(uint32_t taddr, uint32_t (&r)[16])
 {
@@ -323,20 +342,22 @@ __device__ __forceinline__ void box_free() { asm volatile("cp.async.bulk.wait_gr
 __device__ __forceinline__ void box_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 template <bool LORA, class T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_pair(const __grid_constant__ PairTc p)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * PairCfg<LORA>::epi_warps, 1) k_i8_pair(const __grid_constant__ PairTc p)
 {
     using C = PairCfg<LORA>;
     constexpr int BN = C::BN, kStages = C::stages;
     constexpr int kStage = kAtom + BN / 2 * 128;     // token box, half of the weight box
     constexpr int kF = BN;                           // LORA: first column of the fp32 accumulator
     constexpr int NB = C::buffers;                   // integer accumulators
-    constexpr int kCols = BN / 2;                    // columns an epilogue warp takes
+    constexpr int kEpiWarps = C::epi_warps, kThreads = 64 + 32 * kEpiWarps;
+    constexpr int kCols = BN / (kEpiWarps / 4);      // columns an epilogue warp takes
+    constexpr int kBox = 32 * C::box_cols;           // its staged 32 rows
     extern __shared__ __align__(1024) unsigned char sm_dyn[];
     // (the two CTAs' buffers must lie at the same offset: the launch gives both the same base)
     unsigned char *sm = sm_dyn + ((1024 - (smem_u32(sm_dyn) & 1023)) & 1023);
     __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
     __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], mma_drain;
-    __shared__ PairRows tab[LORA ? kPTable : 1];
+    __shared__ std::conditional_t<LORA, SegTable, int> tab;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
 
@@ -353,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 2 * kPEpiWarps);
+            mbar_init(&acc_empty[b], 2 * kEpiWarps);
         }
         mbar_init(&mma_drain, 1);
         abort_flag = 0;
@@ -372,56 +393,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
     const uint32_t tmem = tmem_base;
     pdl_wait();
     pdl_trigger();
-    const int n_tiles = LORA ? p.a.hdr->n_groups : 0;
-    const int n_pairs = LORA ? (n_tiles + 1) / 2 : (p.a.N + 255) / 256;
+    // rows: all of them, or what the segments cover (nothing where the plan found them bad)
+    const int row_begin = LORA ? p.a.seg_off[0] : 0;
+    const int row_end = LORA ? (p.a.hdr->n_groups ? p.a.seg_off[p.a.n_seg] : row_begin) : p.a.N;
+    const int n_pairs = (row_end - row_begin + 255) / 256;
     const int64_t n_units = (int64_t)n_pairs * n_ns;
     int issued = 0;
+    const SegTable *seg_tab = nullptr;
     if constexpr (LORA) {
-        // every tile of the first output slice reports a bad adapter, in whichever CTA it falls
-        for (int64_t i = tid; c0 + i * G < n_units; i += kPThreads) {
-            const PairTile un = pair_tile(c0 + i * G, n_pairs, n_ns);
-            const bool report = rank == 0 && un.ns == 0;
-            if (i < kPTable)
-                tab[i] = pair_lookup(p, un.pair, n_tiles, report);
-            else if (report)
-                pair_lookup(p, un.pair, n_tiles, true);
+        seg_tab = &tab;
+        for (int k = tid; k <= p.a.n_seg && n_pairs; k += kThreads) {
+            const int r0 = p.a.seg_off[k];
+            if (k <= kSegTable)
+                tab.off[k] = r0;
+            if (k < p.a.n_seg) {
+                const bool report = blockIdx.x == 0 && p.a.seg_off[k + 1] > r0;
+                if (k < kSegTable)
+                    tab.ad[k] = seg_lookup(p, k, report);
+                else if (report)
+                    seg_lookup(p, k, true);
+            }
         }
         __syncthreads();
     }
+    const Segments segs = {p, seg_tab, p.a.n_seg <= kSegTable};
 
     if (warp == 0) {
         // ------------------------------------------------ producer (both CTAs)
-        int it = 0, t = 0;
         if (p.test_stall)
             goto done;
         const uint64_t pol_x = policy_evict_first(), pol_w = policy_evict_last();
-        for (int64_t u = c0; u < n_units; u += G, ++t) {
+        int s = 0;
+        uint32_t ph = 1;
+        bool alive = true;
+        // the next stage, free: its token (or s V) box, its weight (or B) box, the pair's barrier
+        unsigned char *as = nullptr, *bs = nullptr;
+        uint32_t bar = 0;
+        auto stage = [&] {
+            alive = warp_wait(&empty_bar[s], ph, &abort_flag, p.a.err, p.wait_ns);
+            as = sm + s * kStage;
+            bs = as + kAtom;
+            bar = map_rank(smem_u32(&full_bar[s]), 0);
+            return alive;
+        };
+        auto sent = [&] {
+            __syncwarp();
+            ++issued;
+            if (++s == kStages) {
+                s = 0;
+                ph ^= 1;
+            }
+        };
+        for (int64_t u = c0; u < n_units && alive; u += G) {
             const PairTile un = pair_tile(u, n_pairs, n_ns);
-            const PairRows pr = pair_rows<LORA>(p, tab, t, un.pair, n_tiles);
-            const int nf0 = LORA ? pr.nf(0) : 0, n_all = nf0 + n_kb + (LORA ? pr.nf(1) : 0);
+            const int tile0 = row_begin + un.pair * 256, row = tile0 + (int)rank * 128;
             const int o0 = un.ns * BN + (int)rank * (BN / 2);
-            const int row = rank ? pr.row[1] : pr.row[0];
-            for (int k = 0; k < n_all; ++k, ++it) {
-                const int s = it % kStages;
-                if (!warp_wait(&empty_bar[s], ((it / kStages) & 1) ^ 1, &abort_flag, p.a.err, p.wait_ns))
-                    goto done;
-                unsigned char *as = sm + s * kStage, *bs = as + kAtom;
-                const int kb = k - nf0;
-                const uint32_t bar = map_rank(smem_u32(&full_bar[s]), 0);
-                if (!LORA || (kb >= 0 && kb < n_kb)) {
-                    if (lane == 0) {
-                        if (rank == 0)
-                            mbar_arrive_expect_tx(&full_bar[s], 2 * kStage);
-                        tma_load_pair(as, &p.map_q, bar, kb * kKB, row, pol_x);
-                        tma_load_pair(bs, &p.map_w, bar, kb * kKB, o0, pol_w);
-                    }
-                } else {
-                    // delta k-block j of a pass: part j % 2 (high, low) of rank columns 64 (j / 2) ..
-                    const int pass = kb < 0 ? 0 : 1;
-                    const int j = pass ? kb - n_kb : k;
-                    const PairAd ad = pr.adapter(pass);
+            // a run's k-blocks: part j % 2 (high, low) of rank columns 64 (j / 2) ..
+            auto delta = [&](const Runs &run) {
+                const SegAd &ad = run.ad;
+                for (int j = 0; j < run.kblocks() && stage(); ++j) {
                     const int c = j >> 1, w = ad.r < 64 ? ad.r : 64;
-                    const bool mine = pr.same() || pass == (int)rank;
                     if (ad.m < 0) {
                         // no view of this rank: all lanes gather the CTA's BN / 2 output rows x 64
                         // rank columns (128-byte swizzle); past r and past d_out zeros
@@ -442,14 +473,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
                         if (rank == 0)
                             mbar_arrive_expect_tx(&full_bar[s],
                                                   (uint32_t)(2 * (kAtom + (ad.m >= 0 ? BN / 2 * w * 2 : 0))));
-                        // (the other adapter's rows are never read, but a box has to arrive)
-                        tma_load_pair(as, &p.map_v, bar, (j & 1) * p.a.kv + c * 64, mine ? row : p.a.N, pol_x);
+                        tma_load_pair(as, &p.map_v, bar, (j & 1) * p.a.kv + c * 64, row, pol_x);
                         if (ad.m >= 0)
                             tma_load_pair(bs, &p.map_b[ad.m], bar, c * 64, (int)(ad.boff >> (4 + ad.m)) + o0, pol_w);
                     }
+                    sent();
                 }
-                __syncwarp();
-                issued = it + 1;
+            };
+            auto base = [&] {
+                for (int kb = 0; kb < n_kb && stage(); ++kb) {
+                    if (lane == 0) {
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(&full_bar[s], 2 * kStage);
+                        tma_load_pair(as, &p.map_q, bar, kb * kKB, row, pol_x);
+                        tma_load_pair(bs, &p.map_w, bar, kb * kKB, o0, pol_w);
+                    }
+                    sent();
+                }
+            };
+            if constexpr (LORA) {
+                Runs run(segs, tile0, min(tile0 + 256, row_end));
+                if (run.next())
+                    delta(run);
+                if (alive)
+                    base();
+                while (alive && run.ad.r && run.next())
+                    delta(run);
+            } else {
+                base();
             }
         }
     } else if (warp == 1) {
@@ -459,8 +510,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
         if (rank == 0 && lane == 0) {
             const uint32_t idesc = idesc_i8(256, BN), idesc_f = idesc_bf16(256, BN);
             const uint64_t a0 = sw128_desc(smem_u32(sm)), b0 = sw128_desc(smem_u32(sm) + kAtom);
-            int s = 0, t = 0, pass_no = 0;
+            int s = 0, pass_no = 0;
             uint32_t ph = 0;
+            bool alive = true;
             auto next = [&] {
                 if (++s == kStages) {
                     s = 0;
@@ -468,44 +520,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
                 }
             };
             auto wait = [&](uint64_t *bar, uint32_t parity) {
-                return mbar_wait(bar, parity, &abort_flag, p.a.err, p.wait_ns);
+                alive = mbar_wait(bar, parity, &abort_flag, p.a.err, p.wait_ns);
+                tc_fence_after();
+                return alive;
             };
-            auto delta = [&](const PairAd &ad, int nf) {
-                for (int j = 0; j < nf; ++j) {
-                    if (!wait(&full_bar[s], ph))
-                        return false;
-                    tc_fence_after();
+            // a pass: its accumulators are free / are complete
+            auto begin = [&] { return wait(&acc_empty[pass_no % NB], ((pass_no / NB) & 1) ^ 1); };
+            auto end = [&] {
+                if (alive)
+                    commit_pair(&acc_full[pass_no % NB]);
+                ++pass_no;
+            };
+            auto delta = [&](const Runs &run) {
+                const int r = run.ad.r, m = run.ad.m;
+                for (int j = 0; j < run.kblocks() && wait(&full_bar[s], ph); ++j) {
                     const uint32_t as = smem_u32(sm + s * kStage), bs = as + kAtom;
-                    const int left = ad.r - (j >> 1) * 64;
+                    const int left = r - (j >> 1) * 64;
                     const int steps = ((left < 64 ? left : 64) + 15) >> 4;
                     for (int i = 0; i < steps; ++i) {
                         // B columns in their view's swizzle
-                        const uint64_t bd = ad.r >= 64 || ad.m < 0 ? sw128_desc(bs + i * 32)
-                                          : (ad.r == 32 ? sw64_desc(bs + i * 32) : sw32_desc(bs));
+                        const uint64_t bd = r >= 64 || m < 0 ? sw128_desc(bs + i * 32)
+                                          : (r == 32 ? sw64_desc(bs + i * 32) : sw32_desc(bs));
                         mma_bf16_pair(tmem + kF, sw128_desc(as + i * 32), bd, idesc_f, (j > 0 || i > 0) ? 1u : 0u);
                     }
                     commit_pair(&empty_bar[s]);
                     next();
                 }
-                return true;
             };
-            for (int64_t u = c0; u < n_units; u += G, ++t) {
-                PairRows pr;
-                if constexpr (LORA)
-                    pr = pair_rows<LORA>(p, tab, t, pair_tile(u, n_pairs, n_ns).pair, n_tiles);
-                const int b = pass_no % NB;
-                if (!wait(&acc_empty[b], ((pass_no / NB) & 1) ^ 1))
-                    goto issued_all;
-                ++pass_no;
-                tc_fence_after();
-                if constexpr (LORA)
-                    if (!delta(pr.adapter(0), pr.nf(0)))
-                        goto issued_all;
-                const uint32_t d = tmem + b * BN;
-                for (int kb = 0; kb < n_kb; ++kb) {
-                    if (!wait(&full_bar[s], ph))
-                        goto issued_all;
-                    tc_fence_after();
+            auto base = [&] {
+                const uint32_t d = tmem + (pass_no % NB) * BN;
+                for (int kb = 0; kb < n_kb && wait(&full_bar[s], ph); ++kb) {
                     const uint64_t at = (uint64_t)(s * (kStage >> 4));
 #pragma unroll
                     for (int i = 0; i < kKB / 32; ++i)
@@ -513,58 +557,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
                     commit_pair(&empty_bar[s]);
                     next();
                 }
-                commit_pair(&acc_full[b]);
+            };
+            for (int64_t u = c0; u < n_units && alive; u += G) {
                 if constexpr (LORA) {
-                    if (pr.nf(1)) {                  // the second tile's own adapter
-                        if (!wait(&acc_empty[0], (pass_no & 1) ^ 1))
-                            goto issued_all;
-                        ++pass_no;
-                        tc_fence_after();
-                        if (!delta(pr.adapter(1), pr.nf(1)))
-                            goto issued_all;
-                        commit_pair(&acc_full[0]);
+                    const int tile0 = row_begin + pair_tile(u, n_pairs, n_ns).pair * 256;
+                    Runs run(segs, tile0, min(tile0 + 256, row_end));
+                    const bool any = run.next();
+                    if (!begin())
+                        break;
+                    if (any)
+                        delta(run);
+                    if (alive)
+                        base();
+                    end();
+                    while (alive && run.ad.r && run.next()) {
+                        if (begin())
+                            delta(run);
+                        end();
                     }
+                } else {
+                    if (!begin())
+                        break;
+                    base();
+                    end();
                 }
             }
-        issued_all:;
         }
         __syncwarp();
     } else {
         // ------------------------------------------------ epilogue (both CTAs)
         const int q = warp & 3;                      // TMEM lane quarter
-        const int half = (warp - 2) >> 2;            // columns [half * kCols, + kCols)
-        const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + half * kCols;
-        unsigned char *const box = sm + kStages * kStage + (warp - 2) * 4096;    // 32 rows x 128 bytes
-        constexpr int kBoxCols = 128 / sizeof(T);
-        int t = 0, pass_no = 0;
-        for (int64_t u = c0; u < n_units; u += G, ++t) {
+        const int part = (warp - 2) >> 2;            // columns [part * kCols, + kCols)
+        const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + part * kCols;
+        unsigned char *const box = sm + kStages * kStage + (warp - 2) * kBox;    // 32 rows
+        constexpr int kBoxCols = C::box_cols / sizeof(T);
+        int pass_no = 0;
+        for (int64_t u = c0; u < n_units; u += G) {
             const PairTile un = pair_tile(u, n_pairs, n_ns);
-            const PairRows pr = pair_rows<LORA>(p, tab, t, un.pair, n_tiles);
-            const int r = q * 32 + lane;
-            const int row = (rank ? pr.row[1] : pr.row[0]) + r;
-            const bool valid = r < (rank ? pr.cnt[1] : pr.cnt[0]);
+            const int tile0 = row_begin + un.pair * 256;
+            const int row0 = tile0 + (int)rank * 128 + q * 32, row = row0 + lane;    // the warp's first, this lane's
+            const bool valid = row < row_end;
             const float sx = valid ? __ldg(p.a.Sx + row) : 0.f;
-            const int row0 = row - lane;             // the warp's first row
-            const int o0 = un.ns * BN + half * kCols;
-            const int n_pass = LORA && pr.nf(1) ? 2 : 1;
+            const int o0 = un.ns * BN + part * kCols;
+            Runs run(segs, tile0, LORA ? min(tile0 + 256, row_end) : 0);
+            bool delta = false, more = false;        // this row has a delta; another pass follows
+            if constexpr (LORA) {
+                more = run.next();
+                delta = valid && segs.ad(segs.of_row(row)).r;
+            }
 #pragma unroll 1
-            for (int pass = 0; pass < n_pass; ++pass, ++pass_no) {
+            for (int pass = 0; pass == 0 || more; ++pass, ++pass_no) {
                 const int b = pass_no % NB;
                 if (!warp_wait(&acc_full[b], (pass_no / NB) & 1, &abort_flag, p.a.err, p.wait_ns))
                     goto done;
                 tc_fence_after();
                 const uint32_t acc = lane_base + b * BN;
                 if constexpr (LORA) {
-                    const bool take = pass == (int)rank || n_pass == 1;
-                    const bool delta = (rank ? pr.ad[1] : pr.ad[0]) & 0xff;
+                    const bool take = valid && (delta ? row >= run.r0 && row < run.r1 : pass == 0);
+                    const bool any_delta = __any_sync(0xffffffffu, take && delta);
                     uint32_t out[kCols / 2];         // bf16 pairs
-                    if (take) {
+                    if (__any_sync(0xffffffffu, take)) {
 #pragma unroll
                         for (int c = 0; c < kCols; c += 16) {
                             uint32_t w[16], f[16];
                             float sw[16];
                             tmem_ld16_raw(acc + c, w);
-                            if (delta)
+                            if (any_delta)
                                 tmem_ld16_raw(acc + kF + c, f);
                             load_sw(p, o0 + c, sw);
                             tmem_wait(w);
@@ -585,22 +643,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
                     __syncwarp();
                     if (lane == 0)
                         remote_arrive(map_rank(smem_u32(&acc_empty[b]), 0));
-                    if (take && __all_sync(0xffffffffu, valid)) {
+                    if (__all_sync(0xffffffffu, take)) {
 #pragma unroll
                         for (int c = 0; c < kCols; c += kBoxCols) {
                             if (lane == 0)
                                 box_free();
                             __syncwarp();
 #pragma unroll
-                            for (int g = 0; g < 8; ++g)
-                                st_shared_v4(smem_u32(box) + sw128_off(lane, g), out[c / 2 + 4 * g], out[c / 2 + 4 * g + 1],
-                                             out[c / 2 + 4 * g + 2], out[c / 2 + 4 * g + 3]);
+                            for (int g = 0; g < 4; ++g)
+                                st_shared_v4(smem_u32(box) + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4), out[c / 2 + 4 * g],
+                                             out[c / 2 + 4 * g + 1], out[c / 2 + 4 * g + 2], out[c / 2 + 4 * g + 3]);
                             fence_async_smem();
                             __syncwarp();
                             if (lane == 0 && o0 + c < p.a.d_out)
                                 box_store(&p.map_y, box, o0 + c, row0);
                         }
-                    } else if (take && valid) {      // a segment's last rows: what follows is not ours
+                    } else if (take) {               // the warp's other rows are another pass's
                         T *y = static_cast<T *>(p.a.Y) + (int64_t)row * p.a.ldy + o0;
 #pragma unroll
                         for (int c = 0; c < kCols; c += 8)
@@ -608,6 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1) k_i8_p
                                 *reinterpret_cast<uint4 *>(y + c) =
                                     make_uint4(out[c / 2], out[c / 2 + 1], out[c / 2 + 2], out[c / 2 + 3]);
                     }
+                    more = more && run.next();
                 } else {
 #pragma unroll 1
                     for (int c = 0; c < kCols; c += kBoxCols) {
@@ -879,7 +938,8 @@ __global__ void __launch_bounds__(kFewThreads) k_i8_few(const __grid_constant__ 
     cluster_sync();                                  // (its sums are read: a CTA may go)
 }
 
-bool encode_y(CUtensorMap *m, void *Y, int32_t dtype, int64_t rows, int64_t cols, int64_t ld)
+// y of dtype: boxes of `bytes` (128 or 64, swizzled alike) x 32 rows
+bool encode_y(CUtensorMap *m, void *Y, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, int bytes)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn)
@@ -890,9 +950,10 @@ bool encode_y(CUtensorMap *m, void *Y, int32_t dtype, int64_t rows, int64_t cols
                                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)ld * es};
-    const cuuint32_t box[2] = {(cuuint32_t)(128 / es), 32};
+    const cuuint32_t box[2] = {(cuuint32_t)(bytes / es), 32};
     const cuuint32_t estr[2] = {1, 1};
-    return fn(m, t, 2, Y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    return fn(m, t, 2, Y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -912,13 +973,13 @@ bool encode_box8(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool LORA, class T> cudaError_t launch_pair(const I8Args &a, int64_t max_tiles, cudaStream_t s, bool *ok)
+template <bool LORA, class T> cudaError_t launch_pair(const I8Args &a, cudaStream_t s, bool *ok)
 {
     using C = PairCfg<LORA>;
     PairTc p = {};
     p.a = a;
     *ok = encode_box8(&p.map_q, a.Q, a.N, a.d_in, a.ldq, 128) && encode_box8(&p.map_w, a.W, a.d_out, a.d_in, a.ldw, C::BN / 2) &&
-          encode_y(&p.map_y, a.Y, a.dtype, a.N, a.d_out, a.ldy);
+          encode_y(&p.map_y, a.Y, a.dtype, a.N, a.d_out, a.ldy, C::box_cols);
     p.sw_vec = ((uintptr_t)a.Sw & 15) == 0;
     if (*ok && LORA) {
         *ok = encode_box(&p.map_v, a.Vb, a.N, 2 * (int64_t)a.kv, a.ldvb, 128);
@@ -928,7 +989,7 @@ template <bool LORA, class T> cudaError_t launch_pair(const I8Args &a, int64_t m
         return cudaSuccess;
     p.wait_ns = wait_bound_ns();
     p.test_stall = test_stall_mode();
-    const int smem = C::stages * (kAtom + C::BN / 2 * 128) + kPEpiWarps * 4096 + 1024;
+    const int smem = C::stages * (kAtom + C::BN / 2 * 128) + C::epi_warps * 32 * C::box_cols + 1024;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -940,8 +1001,7 @@ template <bool LORA, class T> cudaError_t launch_pair(const I8Args &a, int64_t m
         if (dev >= 0 && dev < 64)
             attr_set[dev] = true;
     }
-    const int64_t pairs = LORA ? (max_tiles + 1) / 2 : ((int64_t)a.N + 255) / 256;
-    const int64_t units = pairs * ((a.d_out + C::BN - 1) / C::BN);
+    const int64_t units = ((int64_t)a.N + 255) / 256 * ((a.d_out + C::BN - 1) / C::BN);
     int clusters = sm_count() / 2;
     if (units < clusters)
         clusters = (int)units;
@@ -950,7 +1010,7 @@ template <bool LORA, class T> cudaError_t launch_pair(const I8Args &a, int64_t m
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * clusters);
-    cfg.blockDim = dim3(kPThreads);
+    cfg.blockDim = dim3(64 + 32 * C::epi_warps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
@@ -1055,16 +1115,16 @@ template <class T> cudaError_t launch_any(const I8Args &a, cudaStream_t s, bool 
     case 256:
         return launch_few<256, T>(a, best_split, s, ok);
     default:
-        return launch_pair<false, T>(a, 0, s, ok);
+        return launch_pair<false, T>(a, s, ok);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_linear_i8(const I8Args &a, int max_tiles, cudaStream_t s, bool *ok)
+cudaError_t launch_linear_i8(const I8Args &a, cudaStream_t s, bool *ok)
 {
-    if (a.groups)
-        return launch_pair<true, __nv_bfloat16>(a, max_tiles, s, ok);
+    if (a.seg_off)
+        return launch_pair<true, __nv_bfloat16>(a, s, ok);
     return a.dtype == LORA_BF16 ? launch_any<__nv_bfloat16>(a, s, ok)
          : a.dtype == LORA_F16 ? launch_any<__half>(a, s, ok)
                                : launch_any<float>(a, s, ok);

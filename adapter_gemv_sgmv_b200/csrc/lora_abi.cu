@@ -799,7 +799,7 @@ lora_status lora_linear_i8(const int8_t *Q, int64_t ldq, const float *Sx, const 
     a.d_out = d_out;
     a.err = &static_cast<WsHeader *>(ws)->err;
     bool ok = false;
-    LORA_CUDA(launch_linear_i8(a, 0, (cudaStream_t)stream, &ok));
+    LORA_CUDA(launch_linear_i8(a, (cudaStream_t)stream, &ok));
     return ok ? LORA_OK : LORA_ERR_UNSUPPORTED;
 }
 
@@ -870,15 +870,16 @@ lora_status lora_linear_i8_sgmv(const int8_t *Q, int64_t ldq, const float *Sx, c
     a.d_in = pool->d_in;
     a.d_out = pool->d_out;
     a.err = &hdr->err;
-    a.groups = groups;
-    a.hdr = hdr;
+    a.seg_off = seg_off;
     a.seg_ad = seg_ad;
+    a.n_seg = n_seg;
+    a.hdr = hdr;
     a.pool = pool_dev(pool);
     a.Vb = ta.Vb;
     a.ldvb = ta.ldvb;
     a.kv = L.kv;
     bool ok = false;
-    LORA_CUDA(launch_linear_i8(a, max_tiles, s, &ok));
+    LORA_CUDA(launch_linear_i8(a, s, &ok));
     return ok ? LORA_OK : LORA_ERR_UNSUPPORTED;
 }
 

@@ -325,10 +325,11 @@ struct I8Args {
     int32_t dtype;
     int32_t N, d_in, d_out;
     uint32_t *err;
-    // segments with adapters (groups == nullptr: every row, no adapter)
-    const Group *groups;     // tiles of <= 128 rows, one segment each
-    const WsHeader *hdr;
-    const int32_t *seg_ad;   // -1: no adapter
+    // segments with adapters (seg_off == nullptr: every row, no adapter)
+    const int32_t *seg_off;  // [n_seg + 1]
+    const int32_t *seg_ad;   // [n_seg], -1: no adapter
+    int32_t n_seg;
+    const WsHeader *hdr;     // n_groups == 0: bad segments, nothing to do
     PoolDev pool;
     const __nv_bfloat16 *Vb; // s V as bf16 parts [N, 2 kv] (high, then low from column kv)
     int64_t ldvb;
@@ -336,7 +337,7 @@ struct I8Args {
 };
 
 // *ok: the tensor maps could be encoded (else nothing was launched)
-cudaError_t launch_linear_i8(const I8Args &a, int max_tiles, cudaStream_t s, bool *ok);
+cudaError_t launch_linear_i8(const I8Args &a, cudaStream_t s, bool *ok);
 
 // Workspace bytes of lora_merge (0 for unsupported sizes).
 size_t merge_workspace_size(int32_t d_in, int32_t d_out, int32_t max_rank);

@@ -303,6 +303,35 @@ def test_adapted_many_short_segments():
                  what="adapted, short segments")
 
 
+@pytest.mark.parametrize("n_seg", [511, 512, 513, 700])
+def test_adapted_hundreds_of_segments(n_seg):
+    """About as many segments as the kernel keeps at hand, and more; empty ones among them."""
+    rng = np.random.default_rng(n_seg)
+    d_in, d_out = 128, 264
+    hp = rand_host_pool(rng, [8, 64, 128, 32, 16, 40], d_in, d_out)
+    _run_adapted(rng, hp, rng.integers(0, 4, n_seg), rng.integers(-1, 6, n_seg).astype(np.int32), d_in, d_out, 0.5,
+                 what=f"adapted, {n_seg} segments")
+
+
+def test_adapted_does_not_meet_another_adapters_infinities():
+    """An adapter with infinite B, a NaN token: only the rows that use them are not finite."""
+    rng = np.random.default_rng(21)
+    d_in, d_out, N = 128, 264, 300
+    hp = rand_host_pool(rng, [16, 64, 24], d_in, d_out)
+    hp.B[hp.B_off[1]:hp.B_off[1] + 64 * d_out] = 0x7F80
+    X, x, Q, Sx, Wq, Sw, base = _adapted_inputs(rng, N, d_in, d_out)
+    x = x.clone()
+    x[250, 3] = float("nan")
+    off, ads = np.array([0, 100, 140, 170, N], np.int32), np.array([0, 1, -1, 2], np.int32)
+    Y = torch.ones((N, d_out), dtype=torch.bfloat16, device=DEV)
+    L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, DevPool(hp), _i32(off), _i32(ads), 0.5)
+    finite = torch.isfinite(Y).all(1).cpu().numpy()
+    want = np.ones(N, bool)
+    want[100:140] = False
+    want[250] = False
+    assert np.array_equal(finite, want)
+
+
 def test_adapted_model_shape():
     rng = np.random.default_rng(9)
     d_in, d_out = 4096, 1024
