@@ -121,11 +121,14 @@ __host__ __device__ constexpr uint32_t idesc_i8(int M, int N)
 // ------------------------------------------------------------------ the tiles
 template <bool LORA> struct PairCfg;
 template <> struct PairCfg<false> {
-    static constexpr int BN = 256, stages = 6, buffers = 2, epi_warps = 8, box_cols = 128;   // (bytes)
+    static constexpr int threads() { return 64 + 32 * (epi_warps + help_warps); }
+    static constexpr int BN = 256, stages = 6, buffers = 2, epi_warps = 8, box_cols = 128,     // (bytes)
+                         help_warps = 0;
 };
 template <> struct PairCfg<true> {
+    static constexpr int threads() { return 64 + 32 * (epi_warps + help_warps); }
     // (twice the epilogue warps: nothing runs under them)
-    static constexpr int BN = 256, stages = 5, buffers = 1, epi_warps = 16, box_cols = 64;
+    static constexpr int BN = 256, stages = 5, buffers = 1, epi_warps = 16, box_cols = 64, help_warps = 2;
 };
 
 struct PairTc {
@@ -342,14 +345,14 @@ __device__ __forceinline__ void box_free() { asm volatile("cp.async.bulk.wait_gr
 __device__ __forceinline__ void box_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 template <bool LORA, class T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * PairCfg<LORA>::epi_warps, 1) k_i8_pair(const __grid_constant__ PairTc p)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threads(), 1) k_i8_pair(const __grid_constant__ PairTc p)
 {
     using C = PairCfg<LORA>;
     constexpr int BN = C::BN, kStages = C::stages;
     constexpr int kStage = kAtom + BN / 2 * 128;     // token box, half of the weight box
     constexpr int kF = BN;                           // LORA: first column of the fp32 accumulator
     constexpr int NB = C::buffers;                   // integer accumulators
-    constexpr int kEpiWarps = C::epi_warps, kThreads = 64 + 32 * kEpiWarps;
+    constexpr int kEpiWarps = C::epi_warps, kHelp = C::help_warps, kThreads = C::threads();
     constexpr int kCols = BN / (kEpiWarps / 4);      // columns an epilogue warp takes
     constexpr int kBox = 32 * C::box_cols;           // its staged 32 rows
     extern __shared__ __align__(1024) unsigned char sm_dyn[];
@@ -357,6 +360,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * PairCfg<LO
     unsigned char *sm = sm_dyn + ((1024 - (smem_u32(sm_dyn) & 1023)) & 1023);
     __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
     __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], mma_drain;
+    // a gather into a stage is asked for; the helpers' share of it is in
+    __shared__ __align__(8) uint64_t request_bar[LORA ? kStages : 1], gather_bar[LORA ? kStages : 1];
     __shared__ std::conditional_t<LORA, SegTable, int> tab;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -372,6 +377,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * PairCfg<LO
             mbar_init(&full_bar[s], 1);              // leader's expect_tx, for both CTAs' boxes
             mbar_init(&empty_bar[s], 1);
         }
+        if constexpr (LORA)
+            for (int s = 0; s < kStages; ++s) {
+                mbar_init(&request_bar[s], 1);
+                mbar_init(&gather_bar[s], kHelp);
+            }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 2 * kEpiWarps);
@@ -418,19 +428,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * PairCfg<LO
     }
     const Segments segs = {p, seg_tab, p.a.n_seg <= kSegTable};
 
-    if (warp == 0) {
-        // ------------------------------------------------ producer (both CTAs)
+    if (warp == 0 || warp >= 2 + kEpiWarps) {
+        // ------------------------------------------------ producer (both CTAs) and its helpers
+        // (the last warps share the gathers of B rows and follow the ring for that only)
+        const bool lead = warp == 0;
+        const int share = lead ? 0 : warp - 1 - kEpiWarps;
         if (p.test_stall)
             goto done;
         const uint64_t pol_x = policy_evict_first(), pol_w = policy_evict_last();
         int s = 0;
-        uint32_t ph = 1;
+        uint32_t ph = 1, gathers = 0;                // bit s: parity of stage s's next gather
         bool alive = true;
         // the next stage, free: its token (or s V) box, its weight (or B) box, the pair's barrier
         unsigned char *as = nullptr, *bs = nullptr;
         uint32_t bar = 0;
-        auto stage = [&] {
-            alive = warp_wait(&empty_bar[s], ph, &abort_flag, p.a.err, p.wait_ns);
+        // (a helper follows the lead's requests, not the ring: a barrier's parity tells only two
+        // neighbouring rounds apart, and between gathers it may be any number of them away)
+        auto stage = [&](bool gather = false) {
+            if (lead) {
+                alive = warp_wait(&empty_bar[s], ph, &abort_flag, p.a.err, p.wait_ns);
+                if (gather && lane == 0)
+                    mbar_arrive(&request_bar[s]);
+            } else if (gather) {
+                alive = warp_wait(&request_bar[s], (gathers >> s) & 1, &abort_flag, p.a.err, p.wait_ns);
+            }
             as = sm + s * kStage;
             bs = as + kAtom;
             bar = map_rank(smem_u32(&full_bar[s]), 0);
@@ -448,15 +469,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * PairCfg<LO
             const PairTile un = pair_tile(u, n_pairs, n_ns);
             const int tile0 = row_begin + un.pair * 256, row = tile0 + (int)rank * 128;
             const int o0 = un.ns * BN + (int)rank * (BN / 2);
-            // a run's k-blocks: part j % 2 (high, low) of rank columns 64 (j / 2) ..
+            // a run's k-blocks: part j % 2 (high, low) of rank columns 64 (j / 2) ..; the low
+            // part is multiplied with the B rows that came with the high part
             auto delta = [&](const Runs &run) {
                 const SegAd &ad = run.ad;
-                for (int j = 0; j < run.kblocks() && stage(); ++j) {
+                for (int j = 0; j < run.kblocks(); ++j) {
+                    const bool with_b = (j & 1) == 0, gather = with_b && ad.m < 0;
+                    if (!stage(gather))
+                        return;
                     const int c = j >> 1, w = ad.r < 64 ? ad.r : 64;
-                    if (ad.m < 0) {
-                        // no view of this rank: all lanes gather the CTA's BN / 2 output rows x 64
-                        // rank columns (128-byte swizzle); past r and past d_out zeros
-                        for (int idx = lane; idx < BN / 2 * 8; idx += 32) {
+                    if (gather) {
+                        // no view of this rank: the CTA's BN / 2 output rows x 64 rank columns
+                        // (128-byte swizzle), 16 bytes at a time; past r and past d_out zeros
+                        for (int idx = share * 32 + lane; idx < BN / 2 * 8; idx += 32 * (1 + kHelp)) {
                             const int o = idx >> 3, cc = idx & 7, col = c * 64 + cc * 8;
                             const bool ok = o0 + o < p.a.d_out && col < ad.r;
                             const __nv_bfloat16 *src =
@@ -466,15 +491,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * PairCfg<LO
                         asm volatile("cp.async.wait_all;" ::: "memory");
                         fence_async_smem();
                         __syncwarp();
+                        if (!lead) {
+                            if (lane == 0)
+                                mbar_arrive(&gather_bar[s]);
+                        } else {
+                            alive = warp_wait(&gather_bar[s], (gathers >> s) & 1, &abort_flag, p.a.err, p.wait_ns);
+                        }
+                        gathers ^= 1u << s;
+                        if (!alive)
+                            return;
                     }
-                    if (lane == 0) {
+                    if (lead && lane == 0) {
                         // (the s V boxes leave after the gather is complete in both CTAs, so
                         // the barrier, which waits for both, covers the gathered rows too)
+                        const uint32_t b_bytes = with_b && !gather ? BN / 2 * w * 2 : 0;
                         if (rank == 0)
-                            mbar_arrive_expect_tx(&full_bar[s],
-                                                  (uint32_t)(2 * (kAtom + (ad.m >= 0 ? BN / 2 * w * 2 : 0))));
+                            mbar_arrive_expect_tx(&full_bar[s], 2 * (kAtom + b_bytes));
                         tma_load_pair(as, &p.map_v, bar, (j & 1) * p.a.kv + c * 64, row, pol_x);
-                        if (ad.m >= 0)
+                        if (b_bytes)
                             tma_load_pair(bs, &p.map_b[ad.m], bar, c * 64, (int)(ad.boff >> (4 + ad.m)) + o0, pol_w);
                     }
                     sent();
@@ -482,7 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * PairCfg<LO
             };
             auto base = [&] {
                 for (int kb = 0; kb < n_kb && stage(); ++kb) {
-                    if (lane == 0) {
+                    if (lead && lane == 0) {
                         if (rank == 0)
                             mbar_arrive_expect_tx(&full_bar[s], 2 * kStage);
                         tma_load_pair(as, &p.map_q, bar, kb * kKB, row, pol_x);
@@ -533,8 +567,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * PairCfg<LO
             };
             auto delta = [&](const Runs &run) {
                 const int r = run.ad.r, m = run.ad.m;
+                int s_b = 0;                         // the stage that holds the B rows
                 for (int j = 0; j < run.kblocks() && wait(&full_bar[s], ph); ++j) {
-                    const uint32_t as = smem_u32(sm + s * kStage), bs = as + kAtom;
+                    if ((j & 1) == 0)
+                        s_b = s;
+                    const uint32_t as = smem_u32(sm + s * kStage), bs = smem_u32(sm + s_b * kStage) + kAtom;
                     const int left = r - (j >> 1) * 64;
                     const int steps = ((left < 64 ? left : 64) + 15) >> 4;
                     for (int i = 0; i < steps; ++i) {
@@ -543,7 +580,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * PairCfg<LO
                                           : (r == 32 ? sw64_desc(bs + i * 32) : sw32_desc(bs));
                         mma_bf16_pair(tmem + kF, sw128_desc(as + i * 32), bd, idesc_f, (j > 0 || i > 0) ? 1u : 0u);
                     }
-                    commit_pair(&empty_bar[s]);
+                    if (j & 1) {
+                        commit_pair(&empty_bar[s_b]);
+                        commit_pair(&empty_bar[s]);
+                    }
                     next();
                 }
             };
@@ -1010,7 +1050,7 @@ template <bool LORA, class T> cudaError_t launch_pair(const I8Args &a, cudaStrea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * clusters);
-    cfg.blockDim = dim3(64 + 32 * C::epi_warps);
+    cfg.blockDim = dim3(C::threads());
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
