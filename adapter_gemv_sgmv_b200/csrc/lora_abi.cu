@@ -826,11 +826,7 @@ lora_status lora_linear_i8_sgmv(const int8_t *Q, int64_t ldq, const float *Sx, c
     WsHeader *hdr = at<WsHeader>(ws, L.hdr);
     Group *groups = at<Group>(ws, L.groups);
 
-    // tiles and s V (bf16 high and low parts) as for lora_linear_sgmv
-    TcArgs ta = {};
-    tc_encode_a(ta, pool->A, pool->A_elems, pool->d_in);
-    if (!tc_encode_x(ta, X, N, pool->d_in, ldx))
-        return LORA_ERR_UNSUPPORTED;
+    // tiles, then s V as bf16 high and low parts
     PlanArgs pa = {};
     pa.mode = kModeSgmv;
     pa.N = N;
@@ -841,20 +837,20 @@ lora_status lora_linear_i8_sgmv(const int8_t *Q, int64_t ldq, const float *Sx, c
     pa.group = kTcGroup;
     pa.hdr = hdr;
     LORA_CUDA(launch_plan(pa, s));
-    ta.mode = kModeSgmv;
-    ta.groups = groups;
-    ta.hdr = hdr;
-    ta.seg_ad = seg_ad;
-    ta.max_ads = 1;
-    ta.scale = scale;
-    ta.pool = pool_dev(pool);
-    ta.Vb = at<__nv_bfloat16>(ws, L.V);
-    ta.ldvb = 2 * (int64_t)L.kv;
-    ta.vb_lo = L.kv;
-    ta.allow_none = 1;
-    ta.err = &hdr->err;
-    const int max_tiles = N / kTcGroup + n_seg + 1;
-    LORA_CUDA(launch_tc_shrink(ta, max_tiles, pool->max_rank, s));
+    SplitShrinkArgs va = {};
+    va.groups = groups;
+    va.hdr = hdr;
+    va.seg_ad = seg_ad;
+    va.pool = pool_dev(pool);
+    va.scale = scale;
+    va.Vb = at<__nv_bfloat16>(ws, L.V);
+    va.ldvb = 2 * (int64_t)L.kv;
+    va.vb_lo = L.kv;
+    va.err = &hdr->err;
+    bool ok = false;
+    LORA_CUDA(launch_split_shrink(va, X, ldx, N, N / kTcGroup + n_seg + 1, s, &ok));
+    if (!ok)
+        return LORA_ERR_UNSUPPORTED;
 
     I8Args a = {};
     a.Q = Q;
@@ -875,10 +871,9 @@ lora_status lora_linear_i8_sgmv(const int8_t *Q, int64_t ldq, const float *Sx, c
     a.n_seg = n_seg;
     a.hdr = hdr;
     a.pool = pool_dev(pool);
-    a.Vb = ta.Vb;
-    a.ldvb = ta.ldvb;
+    a.Vb = va.Vb;
+    a.ldvb = va.ldvb;
     a.kv = L.kv;
-    bool ok = false;
     LORA_CUDA(launch_linear_i8(a, s, &ok));
     return ok ? LORA_OK : LORA_ERR_UNSUPPORTED;
 }

@@ -336,6 +336,27 @@ struct I8Args {
     int32_t kv;
 };
 
+// s V of the segments' tiles as bf16 high and low parts (shrink_split.cu)
+struct SplitShrinkArgs {
+    CUtensorMap map_x;       // X [N, d_in], boxes 64 x 128, 128-byte swizzle (this and the next: set by the launcher)
+    CUtensorMap map_a[3];    // A pool as [A_elems / d_in, d_in], boxes of 64 columns x 64 / 32 / 8 rows
+    int32_t a_tma;           // the A maps are valid
+    int32_t split;           // CTAs that share a tile's reduction
+    const Group *groups;     // tiles of <= 128 rows, one segment each
+    const WsHeader *hdr;
+    const int32_t *seg_ad;   // -1: no adapter
+    PoolDev pool;
+    float scale;
+    __nv_bfloat16 *Vb;       // scale * v: high part at Vb[n][c], low part at Vb[n][vb_lo + c]
+    int64_t ldvb;
+    int32_t vb_lo;
+    uint32_t *err;
+    unsigned long long wait_ns;   // bound of every wait (set by the launcher)
+    int32_t test_stall;           // the producer issues nothing (set by the launcher)
+};
+cudaError_t launch_split_shrink(const SplitShrinkArgs &a, const void *X, int64_t ldx, int32_t N, int max_tiles,
+                                cudaStream_t s, bool *ok);
+
 // *ok: the tensor maps could be encoded (else nothing was launched)
 cudaError_t launch_linear_i8(const I8Args &a, cudaStream_t s, bool *ok);
 

@@ -1,0 +1,277 @@
+// s V = s A[a] x for the segments' tiles, as bf16 high and low parts (lora_linear_i8_sgmv):
+//
+//     v[n][j] = s sum_i A[a][j][i] x[n][i],   hi = bf16(v), lo = bf16(v - hi)
+//
+// A tile is at most 128 rows of one segment, its product [128 x d_in] x [d_in x rank].
+// Few tiles leave most SMs idle, and a single CTA takes d_in / 64 k-blocks in a row (44 us
+// for 23 segments of 1535 tokens at d_in 4096), so the reduction is split over the CTAs of
+// a cluster: each multiplies its share (tcgen05, fp32 in tensor memory), leaves its sums in
+// its shared memory, and finishes a share of the rows from all of them, added in the order
+// of the CTAs.  Bound: the reads of x (from HBM for long prompts), and for short ones the
+// chain launch - first loads - exchange - store: 8 us for the case above.
+//
+// 192 threads: warp 0 loads (TMA; A rows at offsets no view reaches with 16-byte copies),
+// warp 1 issues the MMAs, warps 2-5 empty the accumulator.
+
+#include "lora_internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace lora {
+namespace {
+
+constexpr int kVThreads = 192;
+constexpr int kVStage = 2 * kAtom;       // x box 128 rows x 64 columns, A rows (at most 128) x 64
+constexpr int kVStages = 3;              // two CTAs to an SM
+constexpr int kVSmem = kVStages * kVStage + 1024;
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    return a;
+}
+
+__device__ __forceinline__ float4 ld_remote(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr));
+    return v;
+}
+
+__global__ void __launch_bounds__(kVThreads) k_split_shrink(const __grid_constant__ SplitShrinkArgs p)
+{
+    extern __shared__ __align__(1024) unsigned char sm_dyn[];
+    unsigned char *sm = sm_dyn + ((1024 - (smem_u32(sm_dyn) & 1023)) & 1023);
+    __shared__ __align__(8) uint64_t full_bar[kVStages], empty_bar[kVStages], acc_full, mma_drain;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int split = p.split, rank = blockIdx.x % split, tile = blockIdx.x / split;
+    pdl_wait();                                      // the tiles are planned, the workspace is free
+    pdl_trigger();
+    // what ends here ends for the whole cluster: it works on one tile
+    if (tile >= p.hdr->n_groups)
+        return;
+    const Group g = p.groups[tile];
+    const int32_t a = p.seg_ad[g.item];
+    int32_t r = 0;
+    int64_t aoff = 0, boff = 0;
+    if (a == -1)
+        return;
+    if (!pool_adapter_ok(p.pool, a, &r, &aoff, &boff)) {
+        if (tid == 0)
+            atomicOr(p.err, (uint32_t)LORA_ERR_BAD_ADAPTER);
+        return;
+    }
+    const int d_in = p.pool.d_in, n_kb = (d_in + kBK - 1) / kBK, r16 = (r + 15) & ~15;
+    const int k0 = rank * n_kb / split, k1 = (rank + 1) * n_kb / split;
+    const bool view = p.a_tma && aoff % d_in == 0 && aoff / d_in + r <= 0x7fffffffLL;
+    int issued = 0;
+
+    if (tid == 0) {
+        for (int s = 0; s < kVStages; ++s) {
+            mbar_init(&full_bar[s], 33);             // the lead's expect_tx and 32 lanes' copies
+            mbar_init(&empty_bar[s], 1);
+        }
+        mbar_init(&acc_full, 1);
+        mbar_init(&mma_drain, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1)
+        tmem_alloc(&tmem_base, 128);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+
+    if (warp == 0) {
+        const uint64_t pol_x = policy_evict_first(), pol_a = policy_evict_last();
+        for (int k = k0; k < k1 && !p.test_stall; ++k, ++issued) {
+            const int s = issued % kVStages;
+            if (!warp_wait(&empty_bar[s], ((issued / kVStages) & 1) ^ 1, &abort_flag, p.err, p.wait_ns))
+                break;
+            unsigned char *xs = sm + s * kVStage, *as = xs + kAtom;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&full_bar[s], kAtom + (view ? r * 128 : 0));
+                tma_load_2d_hint(xs, &p.map_x, &full_bar[s], k * kBK, g.p0, pol_x);
+                if (view) {
+                    const int row = (int)(aoff / d_in);
+                    int j = 0;
+                    for (; j + 64 <= r; j += 64)
+                        tma_load_2d_hint(as + j * 128, &p.map_a[0], &full_bar[s], k * kBK, row + j, pol_a);
+                    for (; j + 32 <= r; j += 32)
+                        tma_load_2d_hint(as + j * 128, &p.map_a[1], &full_bar[s], k * kBK, row + j, pol_a);
+                    for (; j < r; j += 8)
+                        tma_load_2d_hint(as + j * 128, &p.map_a[2], &full_bar[s], k * kBK, row + j, pol_a);
+                }
+            }
+            __syncwarp();
+            if (!view)
+                for (int idx = lane; idx < r * 8; idx += 32) {
+                    const int j = idx >> 3, c = idx & 7, col = k * kBK + c * 8;
+                    const bool ok = col < d_in;
+                    cp_async16(smem_u32(as) + sw128_off(j, c), p.pool.A + aoff + (ok ? (int64_t)j * d_in + col : 0), ok);
+                }
+            cp_async_arrive(&full_bar[s]);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // (rows r .. r16 - 1 of the A tile hold whatever was there: columns nobody reads)
+            const uint32_t idesc = idesc_bf16(128, r16);
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int k = k0; k < k1; ++k) {
+                if (!(ok = mbar_wait(&full_bar[s], ph, &abort_flag, p.err, p.wait_ns)))
+                    break;
+                fence_async_smem();                  // A may have come by cp.async
+                tc_fence_after();
+                const uint32_t xs = smem_u32(sm + s * kVStage), as = xs + kAtom;
+#pragma unroll
+                for (int i = 0; i < kBK / 16; ++i)
+                    tc_mma(tmem, sw128_desc(xs + i * 32), sw128_desc(as + i * 32), idesc, (k > k0 || i > 0) ? 1u : 0u);
+                tc_commit(&empty_bar[s]);
+                if (++s == kVStages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+            if (ok)
+                tc_commit(&acc_full);
+        }
+    } else {
+        // sums to shared memory as [4 ranks][128 rows][4], in the ring's place: every fill has
+        // been multiplied when the accumulator is full
+        const int q = warp & 3, row = q * 32 + lane;
+        if (warp_wait(&acc_full, 0, &abort_flag, p.err, p.wait_ns)) {
+            tc_fence_after();
+            for (int c = 0; c < r16; c += 32) {      // (128 columns are allocated)
+                float v[32];
+                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c, v);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    if (c + i < r16)
+                        st_shared_v4(smem_u32(sm) + ((c + i) / 4 * 128 + row) * 16, __float_as_uint(v[i]),
+                                     __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
+            }
+            tc_fence_before();
+        }
+    }
+    __syncwarp();
+    if (warp == 0)
+        drain_fills(full_bar, kVStages, issued, p.err, p.wait_ns);
+    if (warp == 1 && lane == 0)
+        drain_mma(&mma_drain, 0, p.err, p.wait_ns);
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 128);
+    }
+    __syncwarp();
+    cluster_sync();
+    bool whole = true;                               // a CTA that gave up has no sums to offer
+    for (int c = 0; c < split; ++c) {
+        int f;
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(f) : "r"(map_rank(smem_u32(&abort_flag), c)));
+        whole &= f == 0;
+    }
+    if (whole) {
+        // 8 ranks of a row at a time, zeros from the rank to the next multiple of 16
+        for (int i = rank * kVThreads + tid; i < 16 * r16; i += split * kVThreads) {
+            const int row = i & 127, o = i >> 7;
+            if (row >= g.cnt)
+                continue;
+            const uint32_t at = smem_u32(sm) + (o * 256 + row) * 16;
+            float v[8] = {};
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < split) {
+                    const float4 x = ld_remote(map_rank(at, c)), y = ld_remote(map_rank(at + 128 * 16, c));
+                    v[0] += x.x;
+                    v[1] += x.y;
+                    v[2] += x.z;
+                    v[3] += x.w;
+                    v[4] += y.x;
+                    v[5] += y.y;
+                    v[6] += y.z;
+                    v[7] += y.w;
+                }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float s0 = o * 8 + j < r ? p.scale * v[j] : 0.f, s1 = o * 8 + j + 1 < r ? p.scale * v[j + 1] : 0.f;
+                const __nv_bfloat162 h = __floats2bfloat162_rn(s0, s1);
+                const float2 back = __bfloat1622float2(h);
+                const __nv_bfloat162 l = __floats2bfloat162_rn(s0 - back.x, s1 - back.y);
+                hi[j / 2] = *reinterpret_cast<const uint32_t *>(&h);
+                lo[j / 2] = *reinterpret_cast<const uint32_t *>(&l);
+            }
+            __nv_bfloat16 *v_row = p.Vb + (int64_t)(g.p0 + row) * p.ldvb + o * 8;
+            *reinterpret_cast<uint4 *>(v_row) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(v_row + p.vb_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+    __syncwarp();
+    cluster_sync();                                  // (its sums are read: a CTA may go)
+}
+
+}  // namespace
+
+cudaError_t launch_split_shrink(const SplitShrinkArgs &a_in, const void *X, int64_t ldx, int32_t N, int max_tiles,
+                                cudaStream_t s, bool *ok)
+{
+    SplitShrinkArgs a = a_in;
+    const int d_in = a.pool.d_in;
+    *ok = encode_box(&a.map_x, X, N, d_in, ldx, 128);
+    if (!*ok)
+        return cudaSuccess;
+    const int64_t rows = a.pool.A_elems / d_in;
+    const int boxes[3] = {64, 32, 8};
+    a.a_tma = rows >= 1 && rows <= 0x7fffffffLL;
+    for (int m = 0; m < 3 && a.a_tma; ++m)
+        a.a_tma = encode_box(&a.map_a[m], a.pool.A, rows, d_in, d_in, boxes[m]);
+    // as many CTAs as two to an SM hold at once, each with eight k-blocks at least
+    const int n_kb = (d_in + kBK - 1) / kBK;
+    a.split = 1;
+    while (a.split < 8 && 2 * a.split * max_tiles <= 2 * sm_count() && n_kb >= 16 * a.split)
+        a.split *= 2;
+    a.wait_ns = wait_bound_ns();
+    a.test_stall = test_stall_mode();
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        if ((e = cudaFuncSetAttribute(k_split_shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, kVSmem)) != cudaSuccess)
+            return e;
+        if (dev >= 0 && dev < 64)
+            attr_set[dev] = true;
+    }
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = a.split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(max_tiles * a.split);
+    cfg.blockDim = dim3(kVThreads);
+    cfg.dynamicSmemBytes = kVSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_split_shrink, a);
+}
+
+}  // namespace lora
