@@ -18,13 +18,13 @@
 // Without adapters two integer accumulators alternate, so a tile's epilogue runs under
 // the next one's products.  The delta (LORA) takes the second half of tensor memory as an
 // fp32 accumulator: bf16 k-blocks of (s v) high and low parts against the adapter's B
-// columns.  The epilogue then empties both into packed registers and lets the next tile
-// start before it stores.  (160 columns, which leave room for two integer accumulators
-// beside the fp32 one, were slower: the kernel is bound by what the SMs read from L2,
-// 10 TB/s, and a tile of 256 x BN reads (256 + BN) / (256 BN) bytes a product.)
-// The two row tiles of a pair may belong to different adapters; the second's delta then
-// makes a pass of its own after the first CTA has emptied its accumulators: a row must
-// never meet another adapter's B, not even with factors of zero, as that B may hold an
+// columns, after the base's.  The epilogue takes the integers into registers while those
+// run and hands their accumulator to the next tile, then the fp32 sums while that one
+// starts.  (160 columns, which leave room for two integer accumulators beside the fp32
+// one, were slower: a tile of 256 x BN reads (256 + BN) / (256 BN) bytes a product.)
+// A tile's rows may belong to different adapters.  Each run of rows with one adapter has
+// k-blocks of its own, multiplied with every other row of the accumulator masked: a row
+// must not meet another adapter's B even with factors of zero, for that B may hold an
 // infinity.
 
 #include "lora_internal.cuh"
@@ -85,12 +85,28 @@ __device__ __forceinline__ void mma_i8_pair(uint32_t d, uint64_t a, uint64_t b, 
         : "memory");
 }
 
-__device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// The rows of D that a delta's MMAs leave alone: bit l of word l / 32, rows 0 - 127 in the
+// leader's tensor memory, 128 - 255 in the other's.
+struct RowMask {
+    uint32_t off[8];
+    __device__ RowMask(int r0, int r1)               // rows outside [r0, r1)
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int lo = min(max(r0 - 32 * i, 0), 32), hi = min(max(r1 - 32 * i, 0), 32);
+            off[i] = ~(uint32_t)((1ull << hi) - (1ull << min(lo, hi)));
+        }
+    }
+};
+
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                              const RowMask &m)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8, %9, %10, %11, %12}, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(m.off[0]), "r"(m.off[1]), "r"(m.off[2]), "r"(m.off[3]),
+          "r"(m.off[4]), "r"(m.off[5]), "r"(m.off[6]), "r"(m.off[7])
         : "memory");
 }
 
@@ -164,8 +180,7 @@ __device__ __forceinline__ PairTile pair_tile(int64_t u, int n_pairs, int n_ns)
 
 // ------------------------------------------------------------- segments (LORA)
 // A tile is 256 consecutive rows, whatever segments they belong to: the base product does
-// not ask.  The delta does: the tile's runs of rows with one adapter make one pass each,
-// and a row is taken from the pass of its own adapter (rows without one from the first).
+// not ask.  The delta does: it walks the tile in runs of rows with one adapter.
 // The segments' bounds and adapters are looked up once, by all threads, when the CTA
 // starts: four dependent loads from global memory each, which every role would otherwise
 // wait for in every tile.
@@ -276,6 +291,13 @@ __device__ __forceinline__ void tmem_ld16_raw(uint32_t taddr, uint32_t (&r)[16])
         : "r"(taddr));
 }
 
+__device__ __forceinline__ void tmem_ld8_raw(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
 // N consecutive columns (a multiple of 16) of this thread's lane, not yet waited for
 template <int N> __device__ __forceinline__ void tmem_ld16s(uint32_t taddr, uint32_t (&r)[N])
 {
@@ -305,11 +327,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// channel scales of outputs o .. o + 15 (zeros past d_out, a multiple of 8)
-__device__ __forceinline__ void load_sw(const PairTc &p, int o, float (&sw)[16])
+// channel scales of outputs o .. o + N - 1 (zeros past d_out, a multiple of 8)
+template <int N> __device__ __forceinline__ void load_sw(const PairTc &p, int o, float (&sw)[N])
 {
 #pragma unroll
-    for (int g = 0; g < 16; g += 8) {
+    for (int g = 0; g < N; g += 8) {
         const float *s = p.a.Sw + o + g;
         if (o + g >= p.a.d_out) {
 #pragma unroll
@@ -359,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
     // (the two CTAs' buffers must lie at the same offset: the launch gives both the same base)
     unsigned char *sm = sm_dyn + ((1024 - (smem_u32(sm_dyn) & 1023)) & 1023);
     __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
-    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], mma_drain;
+    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], f_full, f_empty, mma_drain;
     // a gather into a stage is asked for; the helpers' share of it is in
     __shared__ __align__(8) uint64_t request_bar[LORA ? kStages : 1], gather_bar[LORA ? kStages : 1];
     __shared__ std::conditional_t<LORA, SegTable, int> tab;
@@ -386,6 +408,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 2 * kEpiWarps);
         }
+        mbar_init(&f_full, 1);
+        mbar_init(&f_empty, 2 * kEpiWarps);
         mbar_init(&mma_drain, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -525,17 +549,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
                     sent();
                 }
             };
-            if constexpr (LORA) {
-                Runs run(segs, tile0, min(tile0 + 256, row_end));
-                if (run.next())
+            base();
+            if constexpr (LORA)
+                for (Runs run(segs, tile0, min(tile0 + 256, row_end)); alive && run.next();)
                     delta(run);
-                if (alive)
-                    base();
-                while (alive && run.ad.r && run.next())
-                    delta(run);
-            } else {
-                base();
-            }
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader, one thread)
@@ -544,7 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
         if (rank == 0 && lane == 0) {
             const uint32_t idesc = idesc_i8(256, BN), idesc_f = idesc_bf16(256, BN);
             const uint64_t a0 = sw128_desc(smem_u32(sm)), b0 = sw128_desc(smem_u32(sm) + kAtom);
-            int s = 0, pass_no = 0;
+            int s = 0, t = 0, n_delta = 0;
             uint32_t ph = 0;
             bool alive = true;
             auto next = [&] {
@@ -558,15 +575,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
                 tc_fence_after();
                 return alive;
             };
-            // a pass: its accumulators are free / are complete
-            auto begin = [&] { return wait(&acc_empty[pass_no % NB], ((pass_no / NB) & 1) ^ 1); };
-            auto end = [&] {
-                if (alive)
-                    commit_pair(&acc_full[pass_no % NB]);
-                ++pass_no;
-            };
-            auto delta = [&](const Runs &run) {
+            auto delta = [&](const Runs &run, int tile0) {
                 const int r = run.ad.r, m = run.ad.m;
+                const RowMask mask(run.r0 - tile0, run.r1 - tile0);
                 int s_b = 0;                         // the stage that holds the B rows
                 for (int j = 0; j < run.kblocks() && wait(&full_bar[s], ph); ++j) {
                     if ((j & 1) == 0)
@@ -578,7 +589,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
                         // B columns in their view's swizzle
                         const uint64_t bd = r >= 64 || m < 0 ? sw128_desc(bs + i * 32)
                                           : (r == 32 ? sw64_desc(bs + i * 32) : sw32_desc(bs));
-                        mma_bf16_pair(tmem + kF, sw128_desc(as + i * 32), bd, idesc_f, (j > 0 || i > 0) ? 1u : 0u);
+                        mma_bf16_pair(tmem + kF, sw128_desc(as + i * 32), bd, idesc_f, (j > 0 || i > 0) ? 1u : 0u, mask);
                     }
                     if (j & 1) {
                         commit_pair(&empty_bar[s_b]);
@@ -588,7 +599,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
                 }
             };
             auto base = [&] {
-                const uint32_t d = tmem + (pass_no % NB) * BN;
+                const int b = t % NB;
+                if (!wait(&acc_empty[b], ((t / NB) & 1) ^ 1))
+                    return;
+                const uint32_t d = tmem + b * BN;
                 for (int kb = 0; kb < n_kb && wait(&full_bar[s], ph); ++kb) {
                     const uint64_t at = (uint64_t)(s * (kStage >> 4));
 #pragma unroll
@@ -597,29 +611,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
                     commit_pair(&empty_bar[s]);
                     next();
                 }
+                if (alive)
+                    commit_pair(&acc_full[b]);
             };
-            for (int64_t u = c0; u < n_units && alive; u += G) {
+            for (int64_t u = c0; u < n_units && alive; u += G, ++t) {
+                base();
                 if constexpr (LORA) {
                     const int tile0 = row_begin + pair_tile(u, n_pairs, n_ns).pair * 256;
                     Runs run(segs, tile0, min(tile0 + 256, row_end));
-                    const bool any = run.next();
-                    if (!begin())
+                    if (!alive || !run.next())
+                        continue;
+                    if (!wait(&f_empty, (n_delta & 1) ^ 1))
                         break;
-                    if (any)
-                        delta(run);
+                    ++n_delta;
+                    do
+                        delta(run, tile0);
+                    while (alive && run.next());
                     if (alive)
-                        base();
-                    end();
-                    while (alive && run.ad.r && run.next()) {
-                        if (begin())
-                            delta(run);
-                        end();
-                    }
-                } else {
-                    if (!begin())
-                        break;
-                    base();
-                    end();
+                        commit_pair(&f_full);
                 }
             }
         }
@@ -631,83 +640,88 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
         const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + part * kCols;
         unsigned char *const box = sm + kStages * kStage + (warp - 2) * kBox;    // 32 rows
         constexpr int kBoxCols = C::box_cols / sizeof(T);
-        int pass_no = 0;
-        for (int64_t u = c0; u < n_units; u += G) {
+        int t = 0, n_delta = 0;
+        for (int64_t u = c0; u < n_units; u += G, ++t) {
             const PairTile un = pair_tile(u, n_pairs, n_ns);
             const int tile0 = row_begin + un.pair * 256;
             const int row0 = tile0 + (int)rank * 128 + q * 32, row = row0 + lane;    // the warp's first, this lane's
             const bool valid = row < row_end;
             const float sx = valid ? __ldg(p.a.Sx + row) : 0.f;
-            const int o0 = un.ns * BN + part * kCols;
-            Runs run(segs, tile0, LORA ? min(tile0 + 256, row_end) : 0);
-            bool delta = false, more = false;        // this row has a delta; another pass follows
+            const int o0 = un.ns * BN + part * kCols, b = t % NB;
+            const uint32_t acc = lane_base + b * BN;
             if constexpr (LORA) {
-                more = run.next();
-                delta = valid && segs.ad(segs.of_row(row)).r;
-            }
-#pragma unroll 1
-            for (int pass = 0; pass == 0 || more; ++pass, ++pass_no) {
-                const int b = pass_no % NB;
-                if (!warp_wait(&acc_full[b], (pass_no / NB) & 1, &abort_flag, p.a.err, p.wait_ns))
+                const bool tile_delta = Runs(segs, tile0, min(tile0 + 256, row_end)).next();
+                const bool delta = valid && segs.ad(segs.of_row(row)).r;             // this row's
+                if (!warp_wait(&acc_full[b], (t / NB) & 1, &abort_flag, p.a.err, p.wait_ns))
                     goto done;
                 tc_fence_after();
-                const uint32_t acc = lane_base + b * BN;
-                if constexpr (LORA) {
-                    const bool take = valid && (delta ? row >= run.r0 && row < run.r1 : pass == 0);
-                    const bool any_delta = __any_sync(0xffffffffu, take && delta);
-                    uint32_t out[kCols / 2];         // bf16 pairs
-                    if (__any_sync(0xffffffffu, take)) {
+                uint32_t w[kCols];
+                tmem_ld16s(acc, w);
+                tmem_wait(w);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    remote_arrive(map_rank(smem_u32(&acc_empty[b]), 0));
+                if (tile_delta) {
+                    if (!warp_wait(&f_full, n_delta & 1, &abort_flag, p.a.err, p.wait_ns))
+                        goto done;
+                    ++n_delta;
+                    tc_fence_after();
+                }
+                const bool any_delta = __any_sync(0xffffffffu, delta);
+                uint32_t out[kCols / 2];             // bf16 pairs
 #pragma unroll
-                        for (int c = 0; c < kCols; c += 16) {
-                            uint32_t w[16], f[16];
-                            float sw[16];
-                            tmem_ld16_raw(acc + c, w);
-                            if (any_delta)
-                                tmem_ld16_raw(acc + kF + c, f);
-                            load_sw(p, o0 + c, sw);
-                            tmem_wait(w);
-                            tmem_wait(f);
+                for (int c = 0; c < kCols; c += 8) {
+                    uint32_t f[8] = {};
+                    float sw[8];
+                    if (any_delta)
+                        tmem_ld8_raw(lane_base + kF + c, f);
+                    load_sw(p, o0 + c, sw);
+                    tmem_wait(f);
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                float v0 = (float)(int)w[i] * (sx * sw[i]);
-                                float v1 = (float)(int)w[i + 1] * (sx * sw[i + 1]);
-                                if (delta) {
-                                    v0 += __uint_as_float(f[i]);
-                                    v1 += __uint_as_float(f[i + 1]);
-                                }
-                                out[(c + i) / 2] = pack2(v0, v1, T());
-                            }
+                    for (int i = 0; i < 8; i += 2) {
+                        float v0 = (float)(int)w[c + i] * (sx * sw[i]);
+                        float v1 = (float)(int)w[c + i + 1] * (sx * sw[i + 1]);
+                        if (delta) {                 // (another row's sums may be anything)
+                            v0 += __uint_as_float(f[i]);
+                            v1 += __uint_as_float(f[i + 1]);
                         }
+                        out[(c + i) / 2] = pack2(v0, v1, T());
                     }
+                }
+                if (tile_delta) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        remote_arrive(map_rank(smem_u32(&acc_empty[b]), 0));
-                    if (__all_sync(0xffffffffu, take)) {
+                        remote_arrive(map_rank(smem_u32(&f_empty), 0));
+                }
+                if (__all_sync(0xffffffffu, valid)) {
 #pragma unroll
-                        for (int c = 0; c < kCols; c += kBoxCols) {
-                            if (lane == 0)
-                                box_free();
-                            __syncwarp();
+                    for (int c = 0; c < kCols; c += kBoxCols) {
+                        if (lane == 0)
+                            box_free();
+                        __syncwarp();
 #pragma unroll
-                            for (int g = 0; g < 4; ++g)
-                                st_shared_v4(smem_u32(box) + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4), out[c / 2 + 4 * g],
-                                             out[c / 2 + 4 * g + 1], out[c / 2 + 4 * g + 2], out[c / 2 + 4 * g + 3]);
-                            fence_async_smem();
-                            __syncwarp();
-                            if (lane == 0 && o0 + c < p.a.d_out)
-                                box_store(&p.map_y, box, o0 + c, row0);
-                        }
-                    } else if (take) {               // the warp's other rows are another pass's
-                        T *y = static_cast<T *>(p.a.Y) + (int64_t)row * p.a.ldy + o0;
-#pragma unroll
-                        for (int c = 0; c < kCols; c += 8)
-                            if (o0 + c < p.a.d_out)
-                                *reinterpret_cast<uint4 *>(y + c) =
-                                    make_uint4(out[c / 2], out[c / 2 + 1], out[c / 2 + 2], out[c / 2 + 3]);
+                        for (int g = 0; g < 4; ++g)
+                            st_shared_v4(smem_u32(box) + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4), out[c / 2 + 4 * g],
+                                         out[c / 2 + 4 * g + 1], out[c / 2 + 4 * g + 2], out[c / 2 + 4 * g + 3]);
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && o0 + c < p.a.d_out)
+                            box_store(&p.map_y, box, o0 + c, row0);
                     }
-                    more = more && run.next();
-                } else {
+                } else if (valid) {                  // the segments' last rows: what follows is not ours
+                    T *y = static_cast<T *>(p.a.Y) + (int64_t)row * p.a.ldy + o0;
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 8)
+                        if (o0 + c < p.a.d_out)
+                            *reinterpret_cast<uint4 *>(y + c) =
+                                make_uint4(out[c / 2], out[c / 2 + 1], out[c / 2 + 2], out[c / 2 + 3]);
+                }
+            } else {
+                if (!warp_wait(&acc_full[b], (t / NB) & 1, &abort_flag, p.a.err, p.wait_ns))
+                    goto done;
+                tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < kCols; c += kBoxCols) {
                         uint32_t w[kBoxCols];
@@ -749,7 +763,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
                         if (lane == 0 && row0 < p.a.N && o0 + c < p.a.d_out)
                             box_store(&p.map_y, box, o0 + c, row0);
                     }
-                }
             }
         }
     }
