@@ -35,7 +35,7 @@
 namespace lora {
 namespace {
 
-constexpr int kPNsBlock = 8;            // output slices per block of the tile order
+constexpr int kPNsBlock = 16;           // output slices per block of the tile order
 constexpr int kKB = 128;                // bytes of the reduction per k-block
 
 // -------------------------------------------------------------- pair PTX glue
@@ -138,20 +138,18 @@ __host__ __device__ constexpr uint32_t idesc_i8(int M, int N)
 template <bool LORA> struct PairCfg;
 template <> struct PairCfg<false> {
     static constexpr int threads() { return 64 + 32 * (epi_warps + help_warps); }
-    static constexpr int BN = 256, stages = 6, buffers = 2, epi_warps = 8, box_cols = 128,     // (bytes)
-                         help_warps = 0;
+    static constexpr int BN = 256, stages = 6, buffers = 2, epi_warps = 8, help_warps = 0, box_bytes = 128;
 };
 template <> struct PairCfg<true> {
     static constexpr int threads() { return 64 + 32 * (epi_warps + help_warps); }
-    // (twice the epilogue warps: nothing runs under them)
-    static constexpr int BN = 256, stages = 5, buffers = 1, epi_warps = 16, box_cols = 64, help_warps = 2;
+    static constexpr int BN = 256, stages = 5, buffers = 1, epi_warps = 16, help_warps = 2, box_bytes = 64;
 };
 
 struct PairTc {
     I8Args a;
     CUtensorMap map_q;       // tokens [N, d_in], boxes 128 bytes x 128 rows, 128-byte swizzle
     CUtensorMap map_w;       // weight [d_out, d_in], boxes 128 bytes x BN / 2 rows
-    CUtensorMap map_y;       // y [N, d_out], boxes 128 bytes x 32 rows (written)
+    CUtensorMap map_y;       // y [N, d_out], boxes of 64 or 128 bytes x 32 rows (written)
     CUtensorMap map_v;       // LORA: s V as bf16 parts [N, 2 kv], boxes 64 columns x 128 rows
     CUtensorMap map_b[4];    // LORA: B pool as [B_elems / r, r], r = 16 << m, boxes of min(r, 64) x BN / 2 rows
     int32_t b_tma;
@@ -164,18 +162,17 @@ struct PairTile {
     int pair, ns;
 };
 
-// Tile u in the blocked order: block k holds every row pair against slices 8k .. 8k + 7,
+// Tile u in the blocked order: block k holds every row pair against slices 16k .. 16k + 15,
 // row-major inside, so the tiles in flight share a few MB of tokens and weights in L2.
-__device__ __forceinline__ PairTile pair_tile(int64_t u, int n_pairs, int n_ns)
+// (32 bits: 2^31 tiles would be 2^47 outputs; the 64-bit divisions of every tile took
+// the producer longer than a stage)
+__device__ __forceinline__ PairTile pair_tile(uint32_t u, uint32_t n_pairs, uint32_t n_ns)
 {
-    const int64_t per_blk = (int64_t)n_pairs * kPNsBlock;
-    const int blk = (int)(u / per_blk);
-    const int64_t rem = u - blk * per_blk;
-    const int nsb = min(kPNsBlock, n_ns - blk * kPNsBlock);
-    PairTile t;
-    t.pair = (int)(rem / nsb);
-    t.ns = blk * kPNsBlock + (int)(rem - (int64_t)t.pair * nsb);
-    return t;
+    const uint32_t per_blk = n_pairs * kPNsBlock;
+    const uint32_t blk = u / per_blk, rem = u - blk * per_blk;
+    const uint32_t nsb = min((uint32_t)kPNsBlock, n_ns - blk * kPNsBlock);
+    const uint32_t pair = rem / nsb;
+    return {(int)pair, (int)(blk * kPNsBlock + rem - pair * nsb)};
 }
 
 // ------------------------------------------------------------- segments (LORA)
@@ -327,34 +324,53 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// channel scales of outputs o .. o + N - 1 (zeros past d_out, a multiple of 8)
+// byte offset of 16-byte chunk c (0..3) of row i inside a 64-byte-swizzled box
+__device__ __forceinline__ uint32_t sw64_off(int i, int c) { return (uint32_t)(i * 64 + ((c ^ ((i >> 1) & 3)) << 4)); }
+
+// a b, two at a time
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<unsigned long long *>(&d))
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+    return d;
+}
+
+// sums i, j of outputs with channel scales a, b, in fp32
+__device__ __forceinline__ float2 scaled(uint32_t i, uint32_t j, float sx, float a, float b)
+{
+    return mul2(make_float2((float)(int)i, (float)(int)j), mul2(make_float2(sx, sx), make_float2(a, b)));
+}
+
+// channel scales of outputs o .. o + N - 1 (past d_out, a multiple of 8, some others':
+// those outputs are not written).  All loads leave together: with a branch and a wait for
+// every 16 of them they took a microsecond of each tile.
 template <int N> __device__ __forceinline__ void load_sw(const PairTc &p, int o, float (&sw)[N])
 {
+    if (p.sw_vec) {
 #pragma unroll
-    for (int g = 0; g < N; g += 8) {
-        const float *s = p.a.Sw + o + g;
-        if (o + g >= p.a.d_out) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                sw[g + i] = 0.f;
-        } else if (p.sw_vec) {
+        for (int g = 0; g < N; g += 8) {
+            const float4 *s = reinterpret_cast<const float4 *>(p.a.Sw + min(o + g, p.a.d_out - 8));
 #pragma unroll
             for (int i = 0; i < 8; i += 4) {
-                const float4 v = __ldg(reinterpret_cast<const float4 *>(s + i));
+                const float4 v = __ldg(s + i / 4);
                 sw[g + i] = v.x;
                 sw[g + i + 1] = v.y;
                 sw[g + i + 2] = v.z;
                 sw[g + i + 3] = v.w;
             }
-        } else {
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < N; g += 8)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                sw[g + i] = __ldg(s + i);
-        }
+                sw[g + i] = __ldg(p.a.Sw + min(o + g, p.a.d_out - 8) + i);
     }
 }
 
-// A warp's box of 32 rows x 128 bytes in shared memory to y; the box may be written again
+// A warp's box of 32 rows in shared memory to y; the box may be written again
 // after box_free().
 __device__ __forceinline__ void box_store(const CUtensorMap *map, const void *box, int x, int y)
 {
@@ -376,7 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
     constexpr int NB = C::buffers;                   // integer accumulators
     constexpr int kEpiWarps = C::epi_warps, kHelp = C::help_warps, kThreads = C::threads();
     constexpr int kCols = BN / (kEpiWarps / 4);      // columns an epilogue warp takes
-    constexpr int kBox = 32 * C::box_cols;           // its staged 32 rows
+    constexpr int kBox = 32 * C::box_bytes, kBoxCols = C::box_bytes / sizeof(T);    // staged: 32 rows
     extern __shared__ __align__(1024) unsigned char sm_dyn[];
     // (the two CTAs' buffers must lie at the same offset: the launch gives both the same base)
     unsigned char *sm = sm_dyn + ((1024 - (smem_u32(sm_dyn) & 1023)) & 1023);
@@ -431,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
     const int row_begin = LORA ? p.a.seg_off[0] : 0;
     const int row_end = LORA ? (p.a.hdr->n_groups ? p.a.seg_off[p.a.n_seg] : row_begin) : p.a.N;
     const int n_pairs = (row_end - row_begin + 255) / 256;
-    const int64_t n_units = (int64_t)n_pairs * n_ns;
+    const uint32_t n_units = (uint32_t)n_pairs * n_ns;
     int issued = 0;
     const SegTable *seg_tab = nullptr;
     if constexpr (LORA) {
@@ -489,7 +505,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
                 ph ^= 1;
             }
         };
-        for (int64_t u = c0; u < n_units && alive; u += G) {
+        for (uint32_t u = c0; u < n_units && alive; u += G) {
             const PairTile un = pair_tile(u, n_pairs, n_ns);
             const int tile0 = row_begin + un.pair * 256, row = tile0 + (int)rank * 128;
             const int o0 = un.ns * BN + (int)rank * (BN / 2);
@@ -614,7 +630,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
                 if (alive)
                     commit_pair(&acc_full[b]);
             };
-            for (int64_t u = c0; u < n_units && alive; u += G, ++t) {
+            for (uint32_t u = c0; u < n_units && alive; u += G, ++t) {
                 base();
                 if constexpr (LORA) {
                     const int tile0 = row_begin + pair_tile(u, n_pairs, n_ns).pair * 256;
@@ -639,9 +655,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
         const int part = (warp - 2) >> 2;            // columns [part * kCols, + kCols)
         const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + part * kCols;
         unsigned char *const box = sm + kStages * kStage + (warp - 2) * kBox;    // 32 rows
-        constexpr int kBoxCols = C::box_cols / sizeof(T);
         int t = 0, n_delta = 0;
-        for (int64_t u = c0; u < n_units; u += G, ++t) {
+        for (uint32_t u = c0; u < n_units; u += G, ++t) {
             const PairTile un = pair_tile(u, n_pairs, n_ns);
             const int tile0 = row_begin + un.pair * 256;
             const int row0 = tile0 + (int)rank * 128 + q * 32, row = row0 + lane;    // the warp's first, this lane's
@@ -680,13 +695,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
                     tmem_wait(f);
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
-                        float v0 = (float)(int)w[c + i] * (sx * sw[i]);
-                        float v1 = (float)(int)w[c + i + 1] * (sx * sw[i + 1]);
+                        float2 v = scaled(w[c + i], w[c + i + 1], sx, sw[i], sw[i + 1]);
                         if (delta) {                 // (another row's sums may be anything)
-                            v0 += __uint_as_float(f[i]);
-                            v1 += __uint_as_float(f[i + 1]);
+                            v.x += __uint_as_float(f[i]);
+                            v.y += __uint_as_float(f[i + 1]);
                         }
-                        out[(c + i) / 2] = pack2(v0, v1, T());
+                        out[(c + i) / 2] = pack2(v.x, v.y, T());
                     }
                 }
                 if (tile_delta) {
@@ -703,8 +717,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
                         __syncwarp();
 #pragma unroll
                         for (int g = 0; g < 4; ++g)
-                            st_shared_v4(smem_u32(box) + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4), out[c / 2 + 4 * g],
-                                         out[c / 2 + 4 * g + 1], out[c / 2 + 4 * g + 2], out[c / 2 + 4 * g + 3]);
+                            st_shared_v4(smem_u32(box) + sw64_off(lane, g), out[c / 2 + 4 * g], out[c / 2 + 4 * g + 1],
+                                         out[c / 2 + 4 * g + 2], out[c / 2 + 4 * g + 3]);
                         fence_async_smem();
                         __syncwarp();
                         if (lane == 0 && o0 + c < p.a.d_out)
@@ -723,46 +737,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threa
                     goto done;
                 tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < kCols; c += kBoxCols) {
-                        uint32_t w[kBoxCols];
-                        tmem_ld16s(acc + c, w);
-                        if (lane == 0)
-                            box_free();
-                        tmem_wait(w);
-                        if (c + kBoxCols == kCols) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0)
-                                remote_arrive(map_rank(smem_u32(&acc_empty[b]), 0));
-                        }
+                for (int c = 0; c < kCols; c += kBoxCols) {
+                    uint32_t w[kBoxCols];
+                    float sw[kBoxCols];
+                    tmem_ld16s(acc + c, w);
+                    load_sw(p, o0 + c, sw);
+                    if (lane == 0)
+                        box_free();
+                    tmem_wait(w);
+                    if (c + kBoxCols == kCols) {
+                        tc_fence_before();
                         __syncwarp();
+                        if (lane == 0)
+                            remote_arrive(map_rank(smem_u32(&acc_empty[b]), 0));
+                    }
+                    __syncwarp();
 #pragma unroll
-                        for (int g = 0; g < kBoxCols; g += 16) {
-                            float sw[16], v[16];
-                            load_sw(p, o0 + c + g, sw);
+                    for (int g = 0; g < kBoxCols; g += 16) {
+                        uint32_t x[16];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                v[i] = (float)(int)w[g + i] * (sx * sw[i]);
+                        for (int i = 0; i < 16; i += 2) {
+                            const float2 v = scaled(w[g + i], w[g + i + 1], sx, sw[g + i], sw[g + i + 1]);
                             if constexpr (sizeof(T) == 4) {
-#pragma unroll
-                                for (int i = 0; i < 16; i += 4)
-                                    st_shared_v4(smem_u32(box) + sw128_off(lane, (g + i) / 4), __float_as_uint(v[i]),
-                                                 __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
-                                                 __float_as_uint(v[i + 3]));
+                                x[i] = __float_as_uint(v.x);
+                                x[i + 1] = __float_as_uint(v.y);
                             } else {
-#pragma unroll
-                                for (int i = 0; i < 16; i += 8)
-                                    st_shared_v4(smem_u32(box) + sw128_off(lane, (g + i) / 8), pack2(v[i], v[i + 1], T()),
-                                                 pack2(v[i + 2], v[i + 3], T()), pack2(v[i + 4], v[i + 5], T()),
-                                                 pack2(v[i + 6], v[i + 7], T()));
+                                x[i / 2] = pack2(v.x, v.y, T());
                             }
                         }
-                        fence_async_smem();
-                        __syncwarp();
-                        // (rows past N and outputs past d_out are clipped by the map)
-                        if (lane == 0 && row0 < p.a.N && o0 + c < p.a.d_out)
-                            box_store(&p.map_y, box, o0 + c, row0);
+                        constexpr int n = sizeof(T);         // 16-byte chunks of 16 outputs
+#pragma unroll
+                        for (int i = 0; i < n; ++i)
+                            st_shared_v4(smem_u32(box) + sw128_off(lane, g / 16 * n + i), x[4 * i], x[4 * i + 1],
+                                         x[4 * i + 2], x[4 * i + 3]);
                     }
+                    fence_async_smem();
+                    __syncwarp();
+                    // (rows past N and outputs past d_out are clipped by the map)
+                    if (lane == 0 && row0 < p.a.N && o0 + c < p.a.d_out)
+                        box_store(&p.map_y, box, o0 + c, row0);
+                }
             }
         }
     }
@@ -991,7 +1005,7 @@ __global__ void __launch_bounds__(kFewThreads) k_i8_few(const __grid_constant__ 
     cluster_sync();                                  // (its sums are read: a CTA may go)
 }
 
-// y of dtype: boxes of `bytes` (128 or 64, swizzled alike) x 32 rows
+// y of dtype: boxes of `bytes` (64 or 128, swizzled alike) x 32 rows
 bool encode_y(CUtensorMap *m, void *Y, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, int bytes)
 {
     EncodeTiledFn fn = encode_fn();
@@ -1032,7 +1046,7 @@ template <bool LORA, class T> cudaError_t launch_pair(const I8Args &a, cudaStrea
     PairTc p = {};
     p.a = a;
     *ok = encode_box8(&p.map_q, a.Q, a.N, a.d_in, a.ldq, 128) && encode_box8(&p.map_w, a.W, a.d_out, a.d_in, a.ldw, C::BN / 2) &&
-          encode_y(&p.map_y, a.Y, a.dtype, a.N, a.d_out, a.ldy, C::box_cols);
+          encode_y(&p.map_y, a.Y, a.dtype, a.N, a.d_out, a.ldy, C::box_bytes);
     p.sw_vec = ((uintptr_t)a.Sw & 15) == 0;
     if (*ok && LORA) {
         *ok = encode_box(&p.map_v, a.Vb, a.N, 2 * (int64_t)a.kv, a.ldvb, 128);
@@ -1042,7 +1056,7 @@ template <bool LORA, class T> cudaError_t launch_pair(const I8Args &a, cudaStrea
         return cudaSuccess;
     p.wait_ns = wait_bound_ns();
     p.test_stall = test_stall_mode();
-    const int smem = C::stages * (kAtom + C::BN / 2 * 128) + C::epi_warps * 32 * C::box_cols + 1024;
+    const int smem = C::stages * (kAtom + C::BN / 2 * 128) + C::epi_warps * 32 * C::box_bytes + 1024;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
