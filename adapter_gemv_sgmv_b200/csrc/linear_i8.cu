@@ -135,14 +135,16 @@ __host__ __device__ constexpr uint32_t idesc_i8(int M, int N)
 }
 
 // ------------------------------------------------------------------ the tiles
-template <bool LORA> struct PairCfg;
-template <> struct PairCfg<false> {
-    static constexpr int threads() { return 64 + 32 * (epi_warps + help_warps); }
-    static constexpr int BN = 256, stages = 6, buffers = 2, epi_warps = 8, help_warps = 0, box_bytes = 128;
-};
-template <> struct PairCfg<true> {
-    static constexpr int threads() { return 64 + 32 * (epi_warps + help_warps); }
-    static constexpr int BN = 256, stages = 5, buffers = 1, epi_warps = 16, help_warps = 2, box_bytes = 64;
+template <bool LORA_, int BN_> struct PairCfg {
+    static constexpr bool LORA = LORA_;
+    static constexpr int BN = BN_;                       // outputs of a tile
+    static constexpr int stage = kAtom + BN / 2 * 128;   // token box, half of the weight box
+    static constexpr int stages = LORA ? (BN == 256 ? 5 : 6) : 6;
+    static constexpr int buffers = LORA ? 1 : 2;         // integer accumulators
+    static constexpr int epi_warps = LORA ? 16 : 8, help_warps = LORA ? 2 : 0;
+    static constexpr int box_bytes = LORA ? 64 : 128;    // of a row in an epilogue warp's staged box
+    static constexpr int threads = 64 + 32 * (epi_warps + help_warps);
+    static constexpr int smem = stages * stage + epi_warps * 32 * box_bytes + 1024;
 };
 
 struct PairTc {
@@ -382,15 +384,15 @@ __device__ __forceinline__ void box_store(const CUtensorMap *map, const void *bo
 __device__ __forceinline__ void box_free() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void box_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-template <bool LORA, class T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<LORA>::threads(), 1) k_i8_pair(const __grid_constant__ PairTc p)
+template <class C, class T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_pair(const __grid_constant__ PairTc p)
 {
-    using C = PairCfg<LORA>;
+    constexpr bool LORA = C::LORA;
     constexpr int BN = C::BN, kStages = C::stages;
-    constexpr int kStage = kAtom + BN / 2 * 128;     // token box, half of the weight box
+    constexpr int kStage = C::stage;
     constexpr int kF = BN;                           // LORA: first column of the fp32 accumulator
     constexpr int NB = C::buffers;                   // integer accumulators
-    constexpr int kEpiWarps = C::epi_warps, kHelp = C::help_warps, kThreads = C::threads();
+    constexpr int kEpiWarps = C::epi_warps, kHelp = C::help_warps, kThreads = C::threads;
     constexpr int kCols = BN / (kEpiWarps / 4);      // columns an epilogue warp takes
     constexpr int kBox = 32 * C::box_bytes, kBoxCols = C::box_bytes / sizeof(T);    // staged: 32 rows
     extern __shared__ __align__(1024) unsigned char sm_dyn[];
@@ -1040,15 +1042,14 @@ bool encode_box8(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool LORA, class T> cudaError_t launch_pair(const I8Args &a, cudaStream_t s, bool *ok)
+template <class C, class T> cudaError_t launch_pair(const I8Args &a, cudaStream_t s, bool *ok)
 {
-    using C = PairCfg<LORA>;
     PairTc p = {};
     p.a = a;
     *ok = encode_box8(&p.map_q, a.Q, a.N, a.d_in, a.ldq, 128) && encode_box8(&p.map_w, a.W, a.d_out, a.d_in, a.ldw, C::BN / 2) &&
           encode_y(&p.map_y, a.Y, a.dtype, a.N, a.d_out, a.ldy, C::box_bytes);
     p.sw_vec = ((uintptr_t)a.Sw & 15) == 0;
-    if (*ok && LORA) {
+    if (*ok && C::LORA) {
         *ok = encode_box(&p.map_v, a.Vb, a.N, 2 * (int64_t)a.kv, a.ldvb, 128);
         p.b_tma = encode_b_views(p.map_b, a.pool.B, a.pool.B_elems, C::BN / 2);
     }
@@ -1056,14 +1057,13 @@ template <bool LORA, class T> cudaError_t launch_pair(const I8Args &a, cudaStrea
         return cudaSuccess;
     p.wait_ns = wait_bound_ns();
     p.test_stall = test_stall_mode();
-    const int smem = C::stages * (kAtom + C::BN / 2 * 128) + C::epi_warps * 32 * C::box_bytes + 1024;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        if ((e = cudaFuncSetAttribute(k_i8_pair<LORA, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+        if ((e = cudaFuncSetAttribute(k_i8_pair<C, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem)) != cudaSuccess)
             return e;
         if (dev >= 0 && dev < 64)
             attr_set[dev] = true;
@@ -1077,12 +1077,12 @@ template <bool LORA, class T> cudaError_t launch_pair(const I8Args &a, cudaStrea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * clusters);
-    cfg.blockDim = dim3(C::threads());
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(C::threads);
+    cfg.dynamicSmemBytes = C::smem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_i8_pair<LORA, T>, p);
+    return cudaLaunchKernelEx(&cfg, k_i8_pair<C, T>, p);
 }
 
 template <int NT, class T> cudaError_t launch_few(const I8Args &a, int split, cudaStream_t s, bool *ok)
@@ -1182,7 +1182,7 @@ template <class T> cudaError_t launch_any(const I8Args &a, cudaStream_t s, bool 
     case 256:
         return launch_few<256, T>(a, best_split, s, ok);
     default:
-        return launch_pair<false, T>(a, s, ok);
+        return launch_pair<PairCfg<false, 256>, T>(a, s, ok);
     }
 }
 
@@ -1190,8 +1190,15 @@ template <class T> cudaError_t launch_any(const I8Args &a, cudaStream_t s, bool 
 
 cudaError_t launch_linear_i8(const I8Args &a, cudaStream_t s, bool *ok)
 {
-    if (a.seg_off)
-        return launch_pair<true, __nv_bfloat16>(a, s, ok);
+    if (a.seg_off) {
+        // Tiles of 128 outputs where they still find a free pair of SMs each: the gathers and
+        // the emptying of a tile halve (1535 tokens in 23 segments, 4096 -> 1024: 52 against 57 us
+        // for the whole call), its loads do not.
+        const int64_t pairs = ((int64_t)a.N + 255) / 256;
+        if (pairs * ((a.d_out + 127) / 128) <= sm_count() / 2)
+            return launch_pair<PairCfg<true, 128>, __nv_bfloat16>(a, s, ok);
+        return launch_pair<PairCfg<true, 256>, __nv_bfloat16>(a, s, ok);
+    }
     return a.dtype == LORA_BF16 ? launch_any<__nv_bfloat16>(a, s, ok)
          : a.dtype == LORA_F16 ? launch_any<__half>(a, s, ok)
                                : launch_any<float>(a, s, ok);
