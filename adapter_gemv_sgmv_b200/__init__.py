@@ -417,19 +417,20 @@ def _lib_types():
     return _lib or load(), _types
 
 
-def _one_device(tensors) -> int:
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != dev:
+def _one_device(dev: int, *others: int) -> int:
+    """The tensors' device, given the index of each."""
+    for d in others:
+        if d != dev:
             dev = -1
     if dev < 0:
         raise LoraError("tensors must live on one CUDA device", 1)
     return dev
 
 
-def _rows(t, name: str, n: int, d: int):
-    """Leading dimension of a matrix [n, d] (a single row has none: any that fits will do)."""
-    if t.shape != (n, d):
+def _rows(t, name: str, shape):
+    """Leading dimension of a matrix (a single row has none: any that fits will do)."""
+    n, d = shape
+    if t.shape != shape:
         raise LoraError(f"{name} must be a tensor [{n}, {d}]", 1)
     ld, unit = t.stride()
     if unit != 1 and d > 1:
@@ -452,18 +453,23 @@ def _scales(T, t, n: int, name: str):
 _stream_ws: dict = {}
 
 
-def _stream_workspace(T, nbytes: int, dev: int, raw: int, stream) -> Workspace:
-    """A workspace of this device and stream: calls on two streams never share one.  Under graph
-    capture it is a fresh one from the graph's memory, so that no two graphs share it."""
+def _stream_workspace(T, nbytes: int, dev: int, raw: int, stream):
+    """(workspace, its address, its size) of this device and stream: calls on two streams never
+    share one.  Under graph capture it is a fresh one from the graph's memory, so that no two
+    graphs share it."""
     if stream is not None and raw != T.raw_stream(dev):
         with T.stream(stream):                         # allocated, and freed, in that stream's order
             return _stream_workspace(T, nbytes, dev, raw, None)
     if T.capturing():
-        return Workspace(nbytes, device=f"cuda:{dev}")
+        return _placed(Workspace(nbytes, device=f"cuda:{dev}"))
     ws = _stream_ws.get((dev, raw))
-    if ws is None or ws.nbytes < nbytes:
-        ws = _stream_ws[dev, raw] = Workspace(max(nbytes, 2 * (ws.nbytes if ws else 0)), device=f"cuda:{dev}")
+    if ws is None or ws[2] < nbytes:
+        ws = _stream_ws[dev, raw] = _placed(Workspace(max(nbytes, 2 * (ws[2] if ws else 0)), device=f"cuda:{dev}"))
     return ws
+
+
+def _placed(ws: Workspace):
+    return ws, ws.ptr(), ws.nbytes
 
 
 # Each call below launches on the tensors' device: where that is not the current one, it runs
@@ -472,14 +478,15 @@ def _stream_workspace(T, nbytes: int, dev: int, raw: int, stream) -> Workspace:
 def lora_quant_i8(X, Q, S, stream=None):
     """Q[n] = round(127 X[n] / max|X[n]|) (int8), S[n] = max|X[n]| / 127 for rows of bf16, fp16 or fp32."""
     lib, T = _lib_types()
-    dev = _one_device((X, Q, S))
+    dev = _one_device(X.get_device(), Q.get_device(), S.get_device())
     if T.current_device() != dev:
         with T.device(dev):
             return lora_quant_i8(X, Q, S, stream)
     if X.dim() != 2:
         raise LoraError("X must be a 2-D tensor", 1)
-    n, d = X.shape
-    ldx, ldq = _rows(X, "X", n, d), _rows(Q, "Q", n, d)
+    shape = X.shape
+    n, d = shape
+    ldx, ldq = _rows(X, "X", shape), _rows(Q, "Q", shape)
     if Q.dtype is not T.i8:
         raise LoraError("Q must be int8", 1)
     _scales(T, S, n, "S")
@@ -492,27 +499,29 @@ def lora_quant_i8(X, Q, S, stream=None):
 def _i8_operands(T, Q, Sx, Wq, Sw, Y):
     if Q.dtype is not T.i8 or Wq.dtype is not T.i8 or Q.dim() != 2 or Wq.dim() != 2:
         raise LoraError("Q [N, d_in] and Wq [d_out, d_in] must be int8 matrices", 1)
-    n, d_in = Q.shape
-    d_out = Wq.shape[0]
+    q_shape, w_shape = Q.shape, Wq.shape
+    n, d_in = q_shape
+    d_out, k = w_shape
+    if k != d_in:
+        raise LoraError("Q and Wq disagree on d_in", 1)
     _scales(T, Sx, n, "Sx")
     _scales(T, Sw, d_out, "Sw")
-    return n, d_in, d_out, _rows(Q, "Q", n, d_in), _rows(Wq, "Wq", d_out, d_in), _rows(Y, "Y", n, d_out)
+    return n, d_in, d_out, _rows(Q, "Q", q_shape), _rows(Wq, "Wq", w_shape), _rows(Y, "Y", (n, d_out))
 
 
 def lora_linear_i8(Q, Sx, Wq, Sw, Y, ws: Workspace | None = None, stream=None):
     """Y[n][o] = Sx[n] Sw[o] sum_i Q[n][i] Wq[o][i] for int8 tokens and weight; Y is bf16, fp16 or
     fp32 and overwritten.  Returns the workspace (its error word: lora_get_error)."""
     lib, T = _lib_types()
-    dev = _one_device((Q, Sx, Wq, Sw, Y))
+    dev = _one_device(Q.get_device(), Sx.get_device(), Wq.get_device(), Sw.get_device(), Y.get_device())
     if T.current_device() != dev:
         with T.device(dev):
             return lora_linear_i8(Q, Sx, Wq, Sw, Y, ws, stream)
     n, d_in, d_out, ldq, ldw, ldy = _i8_operands(T, Q, Sx, Wq, Sw, Y)
     raw = T.raw_stream(dev) if stream is None else stream.cuda_stream
-    if ws is None:
-        ws = _stream_workspace(T, 256, dev, raw, stream)
+    ws, at, size = _stream_workspace(T, 256, dev, raw, stream) if ws is None else _placed(ws)
     rc = lib.lora_linear_i8(Q.data_ptr(), ldq, Sx.data_ptr(), Wq.data_ptr(), ldw, Sw.data_ptr(), Y.data_ptr(),
-                            _code(T, Y, "Y"), ldy, n, d_in, d_out, ws.ptr(), ws.nbytes, raw)
+                            _code(T, Y, "Y"), ldy, n, d_in, d_out, at, size, raw)
     if rc:
         raise LoraError("lora_linear_i8", rc)
     return ws
@@ -525,13 +534,14 @@ def lora_linear_i8_sgmv(Q, Sx, X, Wq, Sw, Y, pool, seg_off, seg_ad, scale: float
     X holds the bf16 tokens that Q and Sx are the 8-bit form of; Y is bf16, overwritten inside
     the segments and left alone outside them."""
     lib, T = _lib_types()
-    dev = _one_device((Q, Sx, X, Wq, Sw, Y, seg_off, seg_ad, pool.A, pool.B, pool.A_off, pool.B_off, pool.rank))
+    dev = _one_device(*(t.get_device() for t in (Q, Sx, X, Wq, Sw, Y, seg_off, seg_ad, pool.A, pool.B, pool.A_off,
+                                                 pool.B_off, pool.rank)))
     if T.current_device() != dev:
         with T.device(dev):
             return lora_linear_i8_sgmv(Q, Sx, X, Wq, Sw, Y, pool, seg_off, seg_ad, scale, ws, stream, max_rank)
     n, d_in, d_out, ldq, ldw, ldy = _i8_operands(T, Q, Sx, Wq, Sw, Y)
     ps = make_pool_struct(pool, max_rank)
-    ldx = _rows(X, "X", n, d_in)
+    ldx = _rows(X, "X", (n, d_in))
     if X.dtype is not T.bf16 or Y.dtype is not T.bf16:
         raise LoraError("X and Y must be bf16", 1)
     if d_in != ps.d_in or d_out != ps.d_out:
@@ -543,10 +553,12 @@ def lora_linear_i8_sgmv(Q, Sx, X, Wq, Sw, Y, pool, seg_off, seg_ad, scale: float
     raw = T.raw_stream(dev) if stream is None else stream.cuda_stream
     if ws is None:
         need = lib.lora_workspace_size(OP_LINEAR_I8_SGMV, n, ps.n_adapters, d_in, d_out, ps.max_rank, n_seg, 1)
-        ws = _stream_workspace(T, need, dev, raw, stream)
+        ws, at, size = _stream_workspace(T, need, dev, raw, stream)
+    else:
+        ws, at, size = _placed(ws)
     rc = lib.lora_linear_i8_sgmv(Q.data_ptr(), ldq, Sx.data_ptr(), X.data_ptr(), ldx, Wq.data_ptr(), ldw,
                                  Sw.data_ptr(), Y.data_ptr(), ldy, ctypes.byref(ps), seg_off.data_ptr(),
-                                 seg_ad.data_ptr(), n_seg, n, scale, ws.ptr(), ws.nbytes, raw)
+                                 seg_ad.data_ptr(), n_seg, n, float(scale), at, size, raw)
     if rc:
         raise LoraError("lora_linear_i8_sgmv", rc)
     return ws
@@ -562,7 +574,8 @@ def lora_rope(xs, ys, pos, freqs, interleaved: bool = False, mscale: float = 1.0
     k = len(xs)
     if k == 0 or k != len(ys):
         raise LoraError("one output per input", 1)
-    dev = _one_device((pos, freqs, *xs, *ys))
+    dev = _one_device(pos.get_device(), freqs.get_device(), *[t.get_device() for t in xs],
+                      *[t.get_device() for t in ys])
     if T.current_device() != dev:
         with T.device(dev):
             return lora_rope(xs, ys, pos, freqs, interleaved, mscale, inverse, stream)
@@ -588,7 +601,7 @@ def lora_rope(xs, ys, pos, freqs, interleaved: bool = False, mscale: float = 1.0
         raise LoraError("freqs must be a contiguous fp64 tensor [rot / 2]", 1)
     rc = lib.lora_rope((LoraRopeMat * k)(*args), k, _code(T, x0, "x"), pos.data_ptr(), 8 if pos.dtype is T.i64 else 4,
                        freqs.data_ptr(), n, dim, 2 * freqs.shape[0], 1 if interleaved else 0, 1 if inverse else 0,
-                       mscale, T.raw_stream(dev) if stream is None else stream.cuda_stream)
+                       float(mscale), T.raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise LoraError("lora_rope", rc)
 

@@ -356,7 +356,7 @@ template <int N> __device__ __forceinline__ void load_sw(const PairTc &p, int o,
             const float4 *s = reinterpret_cast<const float4 *>(p.a.Sw + min(o + g, p.a.d_out - 8));
 #pragma unroll
             for (int i = 0; i < 8; i += 4) {
-                const float4 v = __ldg(s + i / 4);
+                const float4 v = s[i / 4];
                 sw[g + i] = v.x;
                 sw[g + i + 1] = v.y;
                 sw[g + i + 2] = v.z;
@@ -368,7 +368,7 @@ template <int N> __device__ __forceinline__ void load_sw(const PairTc &p, int o,
         for (int g = 0; g < N; g += 8)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                sw[g + i] = __ldg(p.a.Sw + min(o + g, p.a.d_out - 8) + i);
+                sw[g + i] = p.a.Sw[min(o + g, p.a.d_out - 8) + i];
     }
 }
 
@@ -663,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_
             const int tile0 = row_begin + un.pair * 256;
             const int row0 = tile0 + (int)rank * 128 + q * 32, row = row0 + lane;    // the warp's first, this lane's
             const bool valid = row < row_end;
-            const float sx = valid ? __ldg(p.a.Sx + row) : 0.f;
+            const float sx = valid ? p.a.Sx[row] : 0.f;
             const int o0 = un.ns * BN + part * kCols, b = t % NB;
             const uint32_t acc = lane_base + b * BN;
             if constexpr (LORA) {
@@ -977,14 +977,14 @@ __global__ void __launch_bounds__(kFewThreads) k_i8_few(const __grid_constant__ 
         float sw[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            sw[i] = __ldg(p.a.Sw + o + i);
+            sw[i] = p.a.Sw[o + i];
         for (int t = rank * per + warp; t < min(nv, (rank + 1) * per); t += kFewThreads / 32) {
             int4 v[8];
 #pragma unroll
             for (int r = 0; r < 8; ++r)
                 if (r < split)
                     v[r] = ld_remote_v4(map_rank(mine + t * 512, r));
-            const float sx = __ldg(p.a.Sx + n0 + t);
+            const float sx = p.a.Sx[n0 + t];
             int4 a = v[0];
 #pragma unroll
             for (int r = 1; r < 8; ++r)

@@ -171,7 +171,7 @@ lora_status check_i8(const int8_t *Q, int64_t ldq, const float *Sx, const int8_t
 {
     if (N < 0 || d_in <= 0 || d_out <= 0 || (N > 0 && (!Q || !Sx)) || !W || !Sw || ldq < d_in || ldw < d_in)
         return LORA_ERR_INVALID_ARG;
-    if (d_in > LORA_MAX_I8_IN || (d_in & 7) || (d_out & 7) || (ldq & 15) || (ldw & 15) || misaligned(Q, 16) ||
+    if (N > LORA_MAX_I8_ROWS || d_out > LORA_MAX_I8_ROWS || d_in > LORA_MAX_I8_IN || (d_in & 7) || (d_out & 7) || (ldq & 15) || (ldw & 15) || misaligned(Q, 16) ||
         misaligned(W, 16) || misaligned(Sx, 4) || misaligned(Sw, 4))
         return LORA_ERR_UNSUPPORTED;
     return LORA_OK;

@@ -31,12 +31,14 @@ template <> struct Vec8<float> { uint4 a, b; };
 template <> struct Vec8<__nv_bfloat16> { uint4 a; };
 template <> struct Vec8<__half> { uint4 a; };
 
+// (from L2: the kernel before this one may still be writing x when this one starts, so
+// nothing read here may come from a cache that it does not reach)
 template <class T> __device__ __forceinline__ Vec8<T> load8(const T *p)
 {
     Vec8<T> v;
-    v.a = __ldg(reinterpret_cast<const uint4 *>(p));
+    v.a = __ldcg(reinterpret_cast<const uint4 *>(p));
     if constexpr (sizeof(T) == 4)
-        v.b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+        v.b = __ldcg(reinterpret_cast<const uint4 *>(p) + 1);
     return v;
 }
 
@@ -326,7 +328,7 @@ template <class T> cudaError_t launch_quant(const QuantArgs &a, cudaStream_t s)
             return cudaErrorInvalidValue;            // (not reached)
         else
             k = k_quant_warp<T, 16>;
-        return launch_rows(k, a, (a.N + kRowWarps - 1) / kRowWarps, 32 * kRowWarps, s);
+        return launch_rows(k, a, (int)(((int64_t)a.N + kRowWarps - 1) / kRowWarps), 32 * kRowWarps, s);
     }
     auto threads = [&](int vpt) { return ((units + vpt - 1) / vpt + 31) & ~31; };
     if (threads(1) <= kRowThreads)

@@ -258,7 +258,7 @@ cudaError_t launch_rope_t(RopeArgs &a, bool vec, bool copy, cudaStream_t s)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.N + a.tokens - 1) / a.tokens);
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.N + a.tokens - 1) / a.tokens));
     cfg.blockDim = dim3((a.cols * a.slots + 31) & ~31);
     cfg.dynamicSmemBytes = sizeof(float2) * a.tokens * a.half;
     cfg.stream = s;

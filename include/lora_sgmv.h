@@ -81,6 +81,7 @@ extern "C" {
 #define LORA_MAX_ADS_PER_REQ 8
 #define LORA_MAX_PROJ 4          /* projections sharing one input (lora_sgmv_shrink_proj, _apply_proj) */
 #define LORA_MAX_I8_IN 65536     /* d_in of the 8-bit projections: sums of 8-bit products stay inside 32 bits */
+#define LORA_MAX_I8_ROWS (1 << 30) /* N and d_out of the 8-bit projections */
 #define LORA_MAX_ROPE_DIM 1024   /* head dimension of lora_rope */
 #define LORA_MAX_ROPE_HEADS 4096 /* heads of all the tensors of one lora_rope call */
 
@@ -298,8 +299,10 @@ LORA_API lora_status lora_quant_i8(const void *X, int32_t dtype, int64_t ldx, in
  * once.  Y is OUTPUT ONLY.  Q [N, d_in] and Wq [d_out, d_in]: device int8,
  * leading dimensions multiples of 16, 16-byte aligned (any values, -128
  * included); Sx fp32 [N], Sw fp32 [d_out], applied as they are (NaN and
- * infinities propagate); Y: device [N, d_out] of `dtype` (lora_dtype), ldy as
- * elsewhere.  d_in and d_out multiples of 8, d_in <= LORA_MAX_I8_IN.  One
+ * infinities propagate; Sx[n] Sw[o] is formed first, so it has to lie in
+ * fp32's normal range for full accuracy); Y: device [N, d_out] of `dtype` (lora_dtype), ldy as
+ * elsewhere.  d_in and d_out multiples of 8, d_in <= LORA_MAX_I8_IN, N and d_out
+ * <= LORA_MAX_I8_ROWS.  One
  * launch from one token to long prompts; a decode batch with adapters follows
  * it with lora_bgmv on the same Y.  Workspace: its header only (the error word,
  * lora_workspace_size(LORA_OP_LINEAR_I8, N, 1, d_in, d_out, 8, 0, 1)).  Needs

@@ -477,3 +477,104 @@ def test_adapted_times_out_and_recovers():
     assert L.lora_get_error(ws) == 0
     want = base + oracle.linear_sgmv(X, np.zeros((d_out, d_in), np.uint16), hp, off, ads, 0.5)
     check_parity(widen(to_host(Y)), want, "adapted after a timeout")
+
+
+# ------------------------------------------------------------- streams, graphs, order
+def test_weight_quantised_right_before_its_product():
+    """The product is launched while the kernel that writes its weight still runs; every round
+    brings another weight (and the tokens' quantisation does not stand between them)."""
+    d_in, d_out = 4096, 2048
+    for N in (1, 300):
+        x = torch.randn(N, d_in, device=DEV).bfloat16()
+        Q, Sx = torch.empty(N, d_in, dtype=torch.int8, device=DEV), torch.empty(N, device=DEV)
+        L.lora_quant_i8(x, Q, Sx)
+        Wq, Sw = torch.empty(d_out, d_in, dtype=torch.int8, device=DEV), torch.empty(d_out, device=DEV)
+        Ws = [torch.randn(d_out, d_in, device=DEV).bfloat16() for _ in range(4)]
+        Ys = [torch.empty(N, d_out, device=DEV) for _ in range(4)]
+        torch.cuda.synchronize()
+        for W, Y in zip(Ws, Ys):
+            L.lora_quant_i8(W, Wq, Sw)
+            L.lora_linear_i8(Q, Sx, Wq, Sw, Y)
+        torch.cuda.synchronize()
+        for W, Y in zip(Ws, Ys):
+            q, s = _quant_ref(W.double().cpu().numpy())
+            want = (Q.double() @ torch.tensor(q, device=DEV).double().t()) * Sx.double()[:, None] * \
+                torch.tensor(s, device=DEV).double()
+            assert float(((Y.double() - want).abs() - want.abs() * 3.001 * 2.0 ** -24).max()) <= 0
+
+
+def test_calls_on_a_given_stream_wait_for_nothing_else():
+    """The stream argument: work on it is ordered with it, not with the current stream."""
+    s = torch.cuda.Stream()
+    x = torch.randn(300, 512, device=DEV).bfloat16()
+    Q, Sx = torch.zeros(300, 512, dtype=torch.int8, device=DEV), torch.zeros(300, device=DEV)
+    W = torch.randint(-127, 128, (264, 512), dtype=torch.int8, device=DEV)
+    Sw = torch.ones(264, device=DEV)
+    Y = torch.zeros(300, 264, device=DEV)
+    torch.cuda.synchronize()
+    L.lora_quant_i8(x, Q, Sx, stream=s)
+    ws = L.lora_linear_i8(Q, Sx, W, Sw, Y, stream=s)
+    assert L.lora_get_error(ws, s) == 0                # synchronises s
+    want = (Q.double() @ W.double().t()) * Sx.double()[:, None]
+    assert float(((Y.double() - want).abs() - want.abs() * 3.001 * 2.0 ** -24).max()) <= 0
+
+
+def test_two_graphs_replayed_at_once():
+    """Graphs captured with the library's own workspaces have one each: replayed side by side on
+    two streams, both are right."""
+    rng = np.random.default_rng(31)
+    d_in, d_out = 1024, 1032
+    hp = rand_host_pool(rng, [64, 128], d_in, d_out)
+    pool = DevPool(hp)
+    jobs = []
+    for k, lens in enumerate(([500, 300], [129, 600])):
+        off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+        X, x, Q, Sx, Wq, Sw, base = _adapted_inputs(rng, int(off[-1]), d_in, d_out)
+        ads = np.array([k, 1 - k], np.int32)
+        want = base + oracle.linear_sgmv(X, np.zeros((d_out, d_in), np.uint16), hp, off, ads, 0.5)
+        Y = torch.zeros((int(off[-1]), d_out), dtype=torch.bfloat16, device=DEV)
+        args = (Q, Sx, x, Wq, Sw, Y, pool, _i32(off), _i32(ads), 0.5)
+        L.lora_linear_i8_sgmv(*args)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            L.lora_linear_i8_sgmv(*args)
+        jobs.append((g, Y, want, torch.cuda.Stream(), args))
+    for g, Y, want, s, args in jobs:
+        Y.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, Y, want, s, args in jobs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for g, Y, want, s, args in jobs:
+        check_parity(widen(to_host(Y)), want, "two graphs")
+
+
+def test_no_tokens():
+    W, Sw = torch.zeros(16, 64, dtype=torch.int8, device=DEV), torch.ones(16, device=DEV)
+    Q, Sx = torch.zeros(0, 64, dtype=torch.int8, device=DEV), torch.zeros(0, device=DEV)
+    L.lora_quant_i8(torch.zeros(0, 64, device=DEV), Q, Sx)
+    Y = torch.zeros(0, 16, device=DEV)
+    assert L.lora_get_error(L.lora_linear_i8(Q, Sx, W, Sw, Y)) == 0
+
+
+@pytest.mark.parametrize("bad", ["type", "shape", "scales", "columns", "device"])
+def test_binding_refuses(bad):
+    Q, Sx = torch.zeros(4, 64, dtype=torch.int8, device=DEV), torch.ones(4, device=DEV)
+    W, Sw = torch.zeros(16, 64, dtype=torch.int8, device=DEV), torch.ones(16, device=DEV)
+    Y = torch.full((4, 16), 2.0, device=DEV)
+    if bad == "type":
+        Q = Q.to(torch.uint8)
+    elif bad == "shape":
+        Y = Y[:, :8]
+    elif bad == "scales":
+        Sx = Sx.double()
+    elif bad == "columns":
+        W = torch.zeros(64, 16, dtype=torch.int8, device=DEV).t()
+    else:
+        Sw = Sw.cpu()
+    with pytest.raises(L.LoraError):
+        L.lora_linear_i8(Q, Sx, W, Sw, Y)
+    assert torch.all(Y == 2)
