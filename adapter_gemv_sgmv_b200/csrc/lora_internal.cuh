@@ -341,7 +341,8 @@ struct SplitShrinkArgs {
     CUtensorMap map_x;       // X [N, d_in], boxes 64 x 128, 128-byte swizzle (this and the next: set by the launcher)
     CUtensorMap map_a[3];    // A pool as [A_elems / d_in, d_in], boxes of 64 columns x 64 / 32 / 8 rows
     int32_t a_tma;           // the A maps are valid
-    int32_t split;           // CTAs that share a tile's reduction
+    int32_t split;           // CTAs that share a tile's reduction (this and the next two: set by the launcher)
+    int32_t stage, stages;   // bytes of a ring stage, stages
     const Group *groups;     // tiles of <= 128 rows, one segment each
     const WsHeader *hdr;
     const int32_t *seg_ad;   // -1: no adapter

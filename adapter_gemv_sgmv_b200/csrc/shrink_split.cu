@@ -20,9 +20,11 @@ namespace lora {
 namespace {
 
 constexpr int kVThreads = 192;
-constexpr int kVStage = 2 * kAtom;       // x box 128 rows x 64 columns, A rows (at most 128) x 64
-constexpr int kVStages = 3;              // two CTAs to an SM
-constexpr int kVSmem = kVStages * kVStage + 1024;
+// A stage is an x box of 128 rows x 64 columns and as many A rows as the pool's ranks reach;
+// as many stages as leave two CTAs to an SM (3 at rank 128, 4 at 64, 6 at 16): a tile's loads
+// are a chain of round trips, and rank 64 with 3 stages took 48 us for 17389 tokens.
+constexpr int kVMaxStages = 6;
+constexpr int kVRing = 110 * 1024;
 
 __device__ __forceinline__ void cluster_sync()
 {
@@ -49,11 +51,12 @@ __global__ void __launch_bounds__(kVThreads) k_split_shrink(const __grid_constan
 {
     extern __shared__ __align__(1024) unsigned char sm_dyn[];
     unsigned char *sm = sm_dyn + ((1024 - (smem_u32(sm_dyn) & 1023)) & 1023);
-    __shared__ __align__(8) uint64_t full_bar[kVStages], empty_bar[kVStages], acc_full, mma_drain;
+    __shared__ __align__(8) uint64_t full_bar[kVMaxStages], empty_bar[kVMaxStages], acc_full, mma_drain;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n_stages = p.stages, stage = p.stage;
     const int split = p.split, rank = blockIdx.x % split, tile = blockIdx.x / split;
     pdl_wait();                                      // the tiles are planned, the workspace is free
     pdl_trigger();
@@ -77,8 +80,8 @@ __global__ void __launch_bounds__(kVThreads) k_split_shrink(const __grid_constan
     int issued = 0;
 
     if (tid == 0) {
-        for (int s = 0; s < kVStages; ++s) {
-            mbar_init(&full_bar[s], 33);             // the lead's expect_tx and 32 lanes' copies
+        for (int s = 0; s < n_stages; ++s) {
+            mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], 1);
         }
         mbar_init(&acc_full, 1);
@@ -95,11 +98,22 @@ __global__ void __launch_bounds__(kVThreads) k_split_shrink(const __grid_constan
 
     if (warp == 0) {
         const uint64_t pol_x = policy_evict_first(), pol_a = policy_evict_last();
+        int s = 0;
+        uint32_t ph = 1;
         for (int k = k0; k < k1 && !p.test_stall; ++k, ++issued) {
-            const int s = issued % kVStages;
-            if (!warp_wait(&empty_bar[s], ((issued / kVStages) & 1) ^ 1, &abort_flag, p.err, p.wait_ns))
+            if (!warp_wait(&empty_bar[s], ph, &abort_flag, p.err, p.wait_ns))
                 break;
-            unsigned char *xs = sm + s * kVStage, *as = xs + kAtom;
+            unsigned char *xs = sm + s * stage, *as = xs + kAtom;
+            if (!view) {
+                for (int idx = lane; idx < r * 8; idx += 32) {
+                    const int j = idx >> 3, c = idx & 7, col = k * kBK + c * 8;
+                    const bool ok = col < d_in;
+                    cp_async16(smem_u32(as) + sw128_off(j, c), p.pool.A + aoff + (ok ? (int64_t)j * d_in + col : 0), ok);
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_async_smem();
+                __syncwarp();
+            }
             if (lane == 0) {
                 mbar_arrive_expect_tx(&full_bar[s], kAtom + (view ? r * 128 : 0));
                 tma_load_2d_hint(xs, &p.map_x, &full_bar[s], k * kBK, g.p0, pol_x);
@@ -115,13 +129,10 @@ __global__ void __launch_bounds__(kVThreads) k_split_shrink(const __grid_constan
                 }
             }
             __syncwarp();
-            if (!view)
-                for (int idx = lane; idx < r * 8; idx += 32) {
-                    const int j = idx >> 3, c = idx & 7, col = k * kBK + c * 8;
-                    const bool ok = col < d_in;
-                    cp_async16(smem_u32(as) + sw128_off(j, c), p.pool.A + aoff + (ok ? (int64_t)j * d_in + col : 0), ok);
-                }
-            cp_async_arrive(&full_bar[s]);
+            if (++s == n_stages) {
+                s = 0;
+                ph ^= 1;
+            }
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -133,14 +144,13 @@ __global__ void __launch_bounds__(kVThreads) k_split_shrink(const __grid_constan
             for (int k = k0; k < k1; ++k) {
                 if (!(ok = mbar_wait(&full_bar[s], ph, &abort_flag, p.err, p.wait_ns)))
                     break;
-                fence_async_smem();                  // A may have come by cp.async
                 tc_fence_after();
-                const uint32_t xs = smem_u32(sm + s * kVStage), as = xs + kAtom;
+                const uint32_t xs = smem_u32(sm + s * stage), as = xs + kAtom;
 #pragma unroll
                 for (int i = 0; i < kBK / 16; ++i)
                     tc_mma(tmem, sw128_desc(xs + i * 32), sw128_desc(as + i * 32), idesc, (k > k0 || i > 0) ? 1u : 0u);
                 tc_commit(&empty_bar[s]);
-                if (++s == kVStages) {
+                if (++s == n_stages) {
                     s = 0;
                     ph ^= 1;
                 }
@@ -168,7 +178,7 @@ __global__ void __launch_bounds__(kVThreads) k_split_shrink(const __grid_constan
     }
     __syncwarp();
     if (warp == 0)
-        drain_fills(full_bar, kVStages, issued, p.err, p.wait_ns);
+        drain_fills(full_bar, n_stages, issued, p.err, p.wait_ns);
     if (warp == 1 && lane == 0)
         drain_mma(&mma_drain, 0, p.err, p.wait_ns);
     __syncthreads();
@@ -244,6 +254,11 @@ cudaError_t launch_split_shrink(const SplitShrinkArgs &a_in, const void *X, int6
     a.split = 1;
     while (a.split < 8 && 2 * a.split * max_tiles <= 2 * sm_count() && n_kb >= 16 * a.split)
         a.split *= 2;
+    // (the sums that take the ring's place need 512 bytes a rank)
+    const int r16 = (a.pool.max_rank + 15) & ~15;
+    a.stage = kAtom + r16 * 128;
+    a.stages = kVRing / a.stage < kVMaxStages ? kVRing / a.stage : kVMaxStages;
+    const int smem = a.stages * a.stage + 1024;
     a.wait_ns = wait_bound_ns();
     a.test_stall = test_stall_mode();
     static bool attr_set[64] = {};
@@ -252,7 +267,7 @@ cudaError_t launch_split_shrink(const SplitShrinkArgs &a_in, const void *X, int6
     if (e != cudaSuccess)
         return e;
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        if ((e = cudaFuncSetAttribute(k_split_shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, kVSmem)) != cudaSuccess)
+        if ((e = cudaFuncSetAttribute(k_split_shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, kVRing + 1024)) != cudaSuccess)
             return e;
         if (dev >= 0 && dev < 64)
             attr_set[dev] = true;
@@ -267,7 +282,7 @@ cudaError_t launch_split_shrink(const SplitShrinkArgs &a_in, const void *X, int6
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(max_tiles * a.split);
     cfg.blockDim = dim3(kVThreads);
-    cfg.dynamicSmemBytes = kVSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
