@@ -19,6 +19,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 namespace lora {
 namespace {
 
@@ -314,9 +316,12 @@ template <class T> cudaError_t launch_quant(const QuantArgs &a, cudaStream_t s)
     // A warp a row wastes no time on block-wide waits and little on the row's own arithmetic,
     // but leaves few rows to few slow warps: 4096 bf16, 256 rows 4.1 us against 2.4 for a block a
     // row, 1024 rows 4.7 for both, 2048 rows 6.8 against 7.8, 17389 rows 38.5 against 64.  fp32
-    // rows above 2048 do not fit its registers.
+    // rows above 2048 do not fit its registers.  fp16 needs more rows: one in 150 has a maximum
+    // of 127 times a small odd number, halves everywhere, and 10 us for its warp (2048 rows of
+    // 4096 13.7 against 7.9, 17389 rows 44 against 60).
     const int per_lane = (units + 31) / 32;
-    if (a.N >= 1024 && per_lane <= (sizeof(T) == 4 ? 8 : 16)) {
+    const int many = std::is_same<T, __half>::value ? 4096 : 1024;
+    if (a.N >= many && per_lane <= (sizeof(T) == 4 ? 8 : 16)) {
         void (*k)(QuantArgs);
         if (per_lane <= 2)
             k = k_quant_warp<T, 2>;
