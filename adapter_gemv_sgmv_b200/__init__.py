@@ -1,8 +1,10 @@
 """Multi-LoRA delta (SGMV / BGMV) for B200 -- Python binding of liblora_sgmv.so.
 
 The binding only marshals arguments (tensor pointers, sizes, the current CUDA
-stream) into the C ABI declared in include/lora_sgmv.h; every step of the
-computation runs in the library's kernels.  There is no fallback: if the
+stream) into the C ABI declared in include/lora_sgmv.h -- from Python with
+ctypes, or, for the short calls of an eager decode step, in a native module
+(csrc/binding.cpp, _native.so); every step of the computation runs in the
+library's kernels.  There is no fallback: if the
 shared library is missing or cannot be loaded, every call raises LoraError.
 
 Tensors: bf16 activations and pools on one CUDA device, int32 metadata, int64
@@ -12,6 +14,7 @@ uint8 CUDA tensor; if none is given, one is taken from a per-device cache.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -393,13 +396,12 @@ _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
 
 
 class _T:
-    """What the calls below look up in torch on every call, found once."""
+    """What lora_linear_i8_sgmv looks up in torch on every call, found once."""
 
     def __init__(self):
         import torch
-        self.i8, self.i32, self.i64 = torch.int8, torch.int32, torch.int64
-        self.bf16, self.f32, self.f64 = torch.bfloat16, torch.float32, torch.float64
-        self.codes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}     # lora_dtype
+        self.i8, self.i32 = torch.int8, torch.int32
+        self.bf16, self.f32 = torch.bfloat16, torch.float32
         self.raw_stream = torch._C._cuda_getCurrentRawStream
         self.current_device = torch._C._cuda_getDevice
         self.capturing = torch.cuda.is_current_stream_capturing
@@ -438,13 +440,6 @@ def _rows(t, name: str, shape):
     return ld if n > 1 else (d + 15) // 16 * 16
 
 
-def _code(T, t, name: str) -> int:
-    code = T.codes.get(t.dtype)
-    if code is None:
-        raise LoraError(f"{name} must be bf16, fp16 or fp32", 2)
-    return code
-
-
 def _scales(T, t, n: int, name: str):
     if t.dtype is not T.f32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise LoraError(f"{name} must be a contiguous fp32 tensor of {n} scales", 1)
@@ -472,28 +467,40 @@ def _placed(ws: Workspace):
     return ws, ws.ptr(), ws.nbytes
 
 
-# Each call below launches on the tensors' device: where that is not the current one, it runs
-# again with that device current.
+def _new_workspace(dev: int, stream) -> Workspace:
+    """A header-sized workspace, allocated (and one day freed) in the stream's order."""
+    if stream is None:
+        return Workspace(256, device=f"cuda:{dev}")
+    with _torch().cuda.stream(stream):
+        return Workspace(256, device=f"cuda:{dev}")
+
+
+_native_module = None
+
+
+def _native():
+    """The native half of the binding, loaded once (built by adapter_gemv_sgmv_b200.build)."""
+    global _native_module
+    if _native_module is None:
+        lib = load()
+        _torch()                                       # the module uses torch's libraries
+        path = os.path.join(_PKG, "_native.so")
+        if not os.path.exists(path):
+            raise LoraError(f"{path} not found; build it with `python -m adapter_gemv_sgmv_b200.build`")
+        spec = importlib.util.spec_from_file_location(__name__ + "._native", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.setup(LoraError, _new_workspace, *(ctypes.cast(f, ctypes.c_void_p).value
+                                             for f in (lib.lora_quant_i8, lib.lora_linear_i8, lib.lora_rope)))
+        _native_module = m
+    return _native_module
+
+
+# Each call below launches on the tensors' device, which need not be the current one.
 
 def lora_quant_i8(X, Q, S, stream=None):
     """Q[n] = round(127 X[n] / max|X[n]|) (int8), S[n] = max|X[n]| / 127 for rows of bf16, fp16 or fp32."""
-    lib, T = _lib_types()
-    dev = _one_device(X.get_device(), Q.get_device(), S.get_device())
-    if T.current_device() != dev:
-        with T.device(dev):
-            return lora_quant_i8(X, Q, S, stream)
-    if X.dim() != 2:
-        raise LoraError("X must be a 2-D tensor", 1)
-    shape = X.shape
-    n, d = shape
-    ldx, ldq = _rows(X, "X", shape), _rows(Q, "Q", shape)
-    if Q.dtype is not T.i8:
-        raise LoraError("Q must be int8", 1)
-    _scales(T, S, n, "S")
-    rc = lib.lora_quant_i8(X.data_ptr(), _code(T, X, "X"), ldx, Q.data_ptr(), ldq, S.data_ptr(), n, d,
-                           T.raw_stream(dev) if stream is None else stream.cuda_stream)
-    if rc:
-        raise LoraError("lora_quant_i8", rc)
+    (_native_module or _native()).quant_i8(X, Q, S, stream)
 
 
 def _i8_operands(T, Q, Sx, Wq, Sw, Y):
@@ -512,19 +519,7 @@ def _i8_operands(T, Q, Sx, Wq, Sw, Y):
 def lora_linear_i8(Q, Sx, Wq, Sw, Y, ws: Workspace | None = None, stream=None):
     """Y[n][o] = Sx[n] Sw[o] sum_i Q[n][i] Wq[o][i] for int8 tokens and weight; Y is bf16, fp16 or
     fp32 and overwritten.  Returns the workspace (its error word: lora_get_error)."""
-    lib, T = _lib_types()
-    dev = _one_device(Q.get_device(), Sx.get_device(), Wq.get_device(), Sw.get_device(), Y.get_device())
-    if T.current_device() != dev:
-        with T.device(dev):
-            return lora_linear_i8(Q, Sx, Wq, Sw, Y, ws, stream)
-    n, d_in, d_out, ldq, ldw, ldy = _i8_operands(T, Q, Sx, Wq, Sw, Y)
-    raw = T.raw_stream(dev) if stream is None else stream.cuda_stream
-    ws, at, size = _stream_workspace(T, 256, dev, raw, stream) if ws is None else _placed(ws)
-    rc = lib.lora_linear_i8(Q.data_ptr(), ldq, Sx.data_ptr(), Wq.data_ptr(), ldw, Sw.data_ptr(), Y.data_ptr(),
-                            _code(T, Y, "Y"), ldy, n, d_in, d_out, at, size, raw)
-    if rc:
-        raise LoraError("lora_linear_i8", rc)
-    return ws
+    return (_native_module or _native()).linear_i8(Q, Sx, Wq, Sw, Y, ws, stream)
 
 
 def lora_linear_i8_sgmv(Q, Sx, X, Wq, Sw, Y, pool, seg_off, seg_ad, scale: float, ws: Workspace | None = None,
@@ -570,40 +565,7 @@ def lora_rope(xs, ys, pos, freqs, interleaved: bool = False, mscale: float = 1.0
 
     ys[i] receives xs[i] rotated by pos * freqs (ys[i] may be xs[i] itself: in place).  freqs: fp64
     [rot / 2] on the device, rot <= dim; pos: int32 or int64 [N].  `inverse` turns back: the gradient."""
-    lib, T = _lib_types()
-    k = len(xs)
-    if k == 0 or k != len(ys):
-        raise LoraError("one output per input", 1)
-    dev = _one_device(pos.get_device(), freqs.get_device(), *[t.get_device() for t in xs],
-                      *[t.get_device() for t in ys])
-    if T.current_device() != dev:
-        with T.device(dev):
-            return lora_rope(xs, ys, pos, freqs, interleaved, mscale, inverse, stream)
-    x0 = xs[0]
-    if x0.dim() != 3:
-        raise LoraError("tensors must be [N, heads, dim]", 1)
-    n, _, dim = x0.shape
-    dt = x0.dtype
-    args = []
-    for x, y in zip(xs, ys):
-        shape = x.shape
-        if len(shape) != 3 or shape[0] != n or shape[2] != dim or y.shape != shape or x.dtype is not dt or \
-                y.dtype is not dt:
-            raise LoraError("tensors [N, heads, dim] of one type, N and dim", 1)
-        xt, xh, xu = x.stride()
-        yt, yh, yu = y.stride()
-        if xu != 1 or yu != 1:
-            raise LoraError("unit stride inside a head", 1)
-        args.append((x.data_ptr(), y.data_ptr(), xt, xh, yt, yh, shape[1]))
-    if (pos.dtype is not T.i64 and pos.dtype is not T.i32) or pos.shape != (n,) or (n > 1 and pos.stride(0) != 1):
-        raise LoraError("pos must be a contiguous int32 or int64 tensor [N]", 1)
-    if freqs.dtype is not T.f64 or freqs.dim() != 1 or not freqs.is_contiguous():
-        raise LoraError("freqs must be a contiguous fp64 tensor [rot / 2]", 1)
-    rc = lib.lora_rope((LoraRopeMat * k)(*args), k, _code(T, x0, "x"), pos.data_ptr(), 8 if pos.dtype is T.i64 else 4,
-                       freqs.data_ptr(), n, dim, 2 * freqs.shape[0], 1 if interleaved else 0, 1 if inverse else 0,
-                       float(mscale), T.raw_stream(dev) if stream is None else stream.cuda_stream)
-    if rc:
-        raise LoraError("lora_rope", rc)
+    (_native_module or _native()).rope(xs, ys, pos, freqs, interleaved, mscale, inverse, stream)
 
 
 def lora_rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, low: float = 1.0,

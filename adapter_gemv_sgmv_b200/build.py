@@ -1,4 +1,5 @@
-"""Build liblora_sgmv.so in-tree with nvcc for sm_100a.
+"""Build liblora_sgmv.so in-tree with nvcc for sm_100a, and _native.so, the binding's
+native marshalling, against the installed torch.
 
     python -m adapter_gemv_sgmv_b200.build [--force]
 
@@ -13,12 +14,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblora_sgmv.so")
+EXT = os.path.join(PKG, "_native.so")
+EXT_SOURCE = os.path.join(CSRC, "binding.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -44,7 +48,32 @@ def stale() -> bool:
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
+def build_native(force: bool = False, verbose: bool = False) -> str:
+    """The native half of the Python binding (host code only)."""
+    if not force and os.path.exists(EXT) and all(
+            os.path.getmtime(f) <= os.path.getmtime(EXT)
+            for f in [EXT_SOURCE, os.path.join(INCLUDE, "lora_sgmv.h")]):
+        return EXT
+    from torch.utils import cpp_extension as ce
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [INCLUDE, sysconfig.get_paths()["include"], *ce.include_paths(), os.path.join(cuda, "include")]
+    lib = [*ce.library_paths(), os.path.join(cuda, "lib64")]
+    import torch
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-isystem{i}" for i in inc[1:]], "-I", inc[0], EXT_SOURCE, *[f"-L{d}" for d in lib],
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-lcudart", f"-Wl,-rpath,{ce.library_paths()[0]}",
+           "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, EXT)
+    return EXT
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    build_native(force, verbose)
     if not force and not stale():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"

@@ -191,3 +191,21 @@ def test_freqs_refusals(kw, code):
     with pytest.raises(L.LoraError) as e:
         L.lora_rope_freqs(**kw)
     assert e.value.code == code
+
+
+# --------------------------------------------------------------- native binding
+def test_native_binding_refuses_on_the_host(lib):
+    """Loaded without a GPU, it refuses what is no CUDA tensor before any CUDA call, as LoraError."""
+    import torch
+    x, q, s = torch.zeros(2, 64), torch.zeros(2, 64, dtype=torch.int8), torch.zeros(2)
+    for call in (lambda: L.lora_quant_i8(x, q, s), lambda: L.lora_quant_i8(None, q, s),
+                 lambda: L.lora_linear_i8(q, s, q, s, x), lambda: L.lora_rope([x], [x], s, s),
+                 lambda: L.lora_rope([], [], s, s), lambda: L.lora_rope([x, x], [x], s, s)):
+        with pytest.raises(L.LoraError) as e:
+            call()
+        assert e.value.code == INVALID
+    with pytest.raises(L.LoraError) as e:
+        L.lora_rope([x] * 5, [x] * 5, s, s)
+    assert e.value.code == UNSUPPORTED
+    with pytest.raises(TypeError):
+        L.lora_rope(3, [x], s, s)
