@@ -53,16 +53,17 @@ struct RopeArgs {
     float sign;                     // -1: inverse
 };
 
-// V elements as loaded (16 bytes, or one element)
-template <class T, int V> struct Raw { uint4 u; };
+// V elements as loaded: 16, 8 or 4 bytes in one access, or one element
+template <int BYTES> struct Words;
+template <> struct Words<16> { using type = uint4; };
+template <> struct Words<8> { using type = uint2; };
+template <> struct Words<4> { using type = uint32_t; };
+template <class T, int V> struct Raw { typename Words<V * sizeof(T)>::type u; };
 template <class T> struct Raw<T, 1> { T u; };
 
 template <class T, int V> __device__ __forceinline__ void get(const T *p, Raw<T, V> &r)
 {
-    if constexpr (V == 1)
-        r.u = *p;
-    else
-        r.u = *reinterpret_cast<const uint4 *>(p);
+    r.u = *reinterpret_cast<const decltype(r.u) *>(p);
 }
 
 template <class T, int V> __device__ __forceinline__ void widen(const Raw<T, V> &r, float *f)
@@ -70,9 +71,9 @@ template <class T, int V> __device__ __forceinline__ void widen(const Raw<T, V> 
     if constexpr (V == 1) {
         f[0] = (float)r.u;
     } else {
-        const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(&r.u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < (int)(V * sizeof(T) / 4); ++i) {
             if constexpr (std::is_same<T, float>::value) {
                 f[i] = __uint_as_float(w[i]);
             } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
@@ -89,17 +90,18 @@ template <class T, int V> __device__ __forceinline__ void widen(const Raw<T, V> 
 
 template <class T, int V> __device__ __forceinline__ void put(T *p, const float *f)
 {
+    Raw<T, V> r;
     if constexpr (V == 1) {
         if constexpr (std::is_same<T, float>::value)
-            p[0] = f[0];
+            r.u = f[0];
         else if constexpr (std::is_same<T, __nv_bfloat16>::value)
-            p[0] = __float2bfloat16_rn(f[0]);
+            r.u = __float2bfloat16_rn(f[0]);
         else
-            p[0] = __float2half_rn(f[0]);
+            r.u = __float2half_rn(f[0]);
     } else {
-        uint32_t w[4];
+        uint32_t *w = reinterpret_cast<uint32_t *>(&r.u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < (int)(V * sizeof(T) / 4); ++i) {
             if constexpr (std::is_same<T, float>::value) {
                 w[i] = __float_as_uint(f[i]);
             } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
@@ -110,8 +112,8 @@ template <class T, int V> __device__ __forceinline__ void put(T *p, const float 
                 w[i] = *reinterpret_cast<const uint32_t *>(&h);
             }
         }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    *reinterpret_cast<decltype(r.u) *>(p) = r.u;
 }
 
 // An item is V pairs of one head (two runs of V elements half a rotation apart;
@@ -238,13 +240,10 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 5 : 4) k_rope(c
     }
 }
 
-template <class T, bool INTER>
-cudaError_t launch_rope_t(RopeArgs &a, bool vec, bool copy, cudaStream_t s)
+template <class T, bool INTER, int V> cudaError_t launch_rope_v(RopeArgs &a, bool copy, cudaStream_t s)
 {
-    constexpr int VW = 16 / sizeof(T);
-    const int V = vec ? VW : 1;
     const int rot = 2 * a.half;
-    a.rot_items = INTER ? (vec ? rot / VW : a.half) : a.half / V;
+    a.rot_items = INTER ? (V > 1 ? rot / V : a.half) : a.half / V;
     a.head_items = a.rot_items + (copy ? (a.dim - rot) / V : 0);
     a.cols = a.head_items < kRopeThreads ? a.head_items : kRopeThreads;
     a.slots = kRopeThreads / a.cols;
@@ -266,12 +265,23 @@ cudaError_t launch_rope_t(RopeArgs &a, bool vec, bool copy, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    return vec ? cudaLaunchKernelEx(&cfg, k_rope<T, VW, INTER>, a) : cudaLaunchKernelEx(&cfg, k_rope<T, 1, INTER>, a);
+    return cudaLaunchKernelEx(&cfg, k_rope<T, V, INTER>, a);
 }
 
-template <class T> cudaError_t launch_rope(RopeArgs &a, bool inter, bool vec, bool copy, cudaStream_t s)
+// v: elements an access may move (a power of two, at most 16 bytes)
+template <class T, bool INTER> cudaError_t launch_rope_t(RopeArgs &a, int v, bool copy, cudaStream_t s)
 {
-    return inter ? launch_rope_t<T, true>(a, vec, copy, s) : launch_rope_t<T, false>(a, vec, copy, s);
+    if constexpr (sizeof(T) == 2)
+        if (v == 8)
+            return launch_rope_v<T, INTER, 8>(a, copy, s);
+    return v >= 4 ? launch_rope_v<T, INTER, 4>(a, copy, s)
+         : v == 2 ? launch_rope_v<T, INTER, 2>(a, copy, s)
+                  : launch_rope_v<T, INTER, 1>(a, copy, s);
+}
+
+template <class T> cudaError_t launch_rope(RopeArgs &a, bool inter, int v, bool copy, cudaStream_t s)
+{
+    return inter ? launch_rope_t<T, true>(a, v, copy, s) : launch_rope_t<T, false>(a, v, copy, s);
 }
 
 }  // namespace
@@ -302,12 +312,14 @@ extern "C" lora_status lora_rope(const lora_rope_mat *mats, int32_t n_mats, int3
         return LORA_ERR_INVALID_ARG;
     if (n_mats > LORA_MAX_PROJ || dim > LORA_MAX_ROPE_DIM || dtype < LORA_BF16 || dtype > LORA_F32)
         return LORA_ERR_UNSUPPORTED;
-    const int es = dtype == LORA_F32 ? 4 : 2, vw = 16 / es;
+    const int es = dtype == LORA_F32 ? 4 : 2;
     if (((uintptr_t)pos & (pos_bytes - 1)) || ((uintptr_t)freq & 7))
         return LORA_ERR_UNSUPPORTED;
     RopeArgs a = {};
-    // 16-byte access: every run of 16 bytes that an item moves starts on a 16-byte boundary
-    bool vec = (interleaved ? rot % vw == 0 : (rot / 2) % vw == 0) && dim % vw == 0, copy = false;
+    // elements an access moves, v: every run of v starts on a boundary of its own size.  (A head of
+    // 72 with 36 rotating allows 4, with 18 none; one element at a time costs 2 to 3 times as much.)
+    uint64_t steps = (interleaved ? rot : rot / 2) | rot | dim, at = 0;
+    bool copy = false;
     for (int i = 0; i < n_mats; ++i) {
         const lora_rope_mat &m = mats[i];
         if (N > 0 && (!m.x || !m.y))
@@ -323,8 +335,8 @@ extern "C" lora_status lora_rope(const lora_rope_mat *mats, int32_t n_mats, int3
         if (((uintptr_t)m.x | (uintptr_t)m.y) & (es - 1))
             return LORA_ERR_UNSUPPORTED;
         copy |= !same && rot < dim;
-        vec &= !((((uintptr_t)m.x | (uintptr_t)m.y) & 15) ||
-                 ((m.x_token | m.x_head | m.y_token | m.y_head) & (vw - 1)));
+        steps |= (uint64_t)(m.x_token | m.x_head | m.y_token | m.y_head);
+        at |= (uintptr_t)m.x | (uintptr_t)m.y;
         a.mat[i] = {m.x, m.y, m.x_token, m.x_head, m.y_token, m.y_head, a.heads, 0};
         if (m.heads > LORA_MAX_ROPE_HEADS || (a.heads += m.heads) > LORA_MAX_ROPE_HEADS)
             return LORA_ERR_UNSUPPORTED;
@@ -342,9 +354,12 @@ extern "C" lora_status lora_rope(const lora_rope_mat *mats, int32_t n_mats, int3
     a.sign = inverse ? -1.f : 1.f;
     cudaStream_t s = (cudaStream_t)stream;
     const bool inter = interleaved != 0;
-    const cudaError_t e = dtype == LORA_BF16 ? launch_rope<__nv_bfloat16>(a, inter, vec, copy, s)
-                        : dtype == LORA_F16 ? launch_rope<__half>(a, inter, vec, copy, s)
-                                            : launch_rope<float>(a, inter, vec, copy, s);
+    int v = 16 / es;
+    while (v > 1 && ((steps & (v - 1)) || (at & (v * es - 1))))
+        v /= 2;
+    const cudaError_t e = dtype == LORA_BF16 ? launch_rope<__nv_bfloat16>(a, inter, v, copy, s)
+                        : dtype == LORA_F16 ? launch_rope<__half>(a, inter, v, copy, s)
+                                            : launch_rope<float>(a, inter, v, copy, s);
     return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }
 
