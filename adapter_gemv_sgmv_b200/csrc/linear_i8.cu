@@ -211,7 +211,7 @@ __device__ SegAd seg_lookup(const PairTc &p, int k, bool report)
     }
     // (the view's row index of the last box has to fit 32 bits)
     int m = b_map(r);
-    if (m >= 0 && (!((p.b_tma >> m) & 1) || bo % r != 0 || bo / r + p.a.d_out + 512 > 0x7fffffffLL))
+    if (m >= 0 && (!((p.b_tma >> m) & 1) || (bo & (r - 1)) || (bo >> (4 + m)) + p.a.d_out + 512 > 0x7fffffffLL))
         m = -1;
     x.boff = bo;
     x.a = a;
@@ -399,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_
     // (the two CTAs' buffers must lie at the same offset: the launch gives both the same base)
     unsigned char *sm = sm_dyn + ((1024 - (smem_u32(sm_dyn) & 1023)) & 1023);
     __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
-    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], f_full, f_empty, mma_drain;
+    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], f_full, f_empty, mma_drain, tab_full;
     // a gather into a stage is asked for; the helpers' share of it is in
     __shared__ __align__(8) uint64_t request_bar[LORA ? kStages : 1], gather_bar[LORA ? kStages : 1];
     __shared__ std::conditional_t<LORA, SegTable, int> tab;
@@ -427,6 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_
             mbar_init(&acc_empty[b], 2 * kEpiWarps);
         }
         mbar_init(&f_full, 1);
+        mbar_init(&tab_full, kThreads - 32);
         mbar_init(&f_empty, 2 * kEpiWarps);
         mbar_init(&mma_drain, 1);
         abort_flag = 0;
@@ -454,7 +455,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_
     const SegTable *seg_tab = nullptr;
     if constexpr (LORA) {
         seg_tab = &tab;
-        for (int k = tid; k <= p.a.n_seg && n_pairs; k += kThreads) {
+        // (the producer warp does not look, and starts with the base's loads; whoever reads the
+        // table waits for tab_full first)
+        for (int k = tid - 32; k <= p.a.n_seg && n_pairs && warp; k += kThreads - 32) {
             const int r0 = p.a.seg_off[k];
             if (k <= kSegTable)
                 tab.off[k] = r0;
@@ -466,7 +469,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_
                     seg_lookup(p, k, true);
             }
         }
-        __syncthreads();
+        if (warp)
+            mbar_arrive(&tab_full);
     }
     const Segments segs = {p, seg_tab, p.a.n_seg <= kSegTable};
 
@@ -568,9 +572,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_
                 }
             };
             base();
-            if constexpr (LORA)
+            if constexpr (LORA) {
+                if (u == c0 && alive)
+                    alive = warp_wait(&tab_full, 0, &abort_flag, p.a.err, p.wait_ns);
+                if (!alive)
+                    break;
                 for (Runs run(segs, tile0, min(tile0 + 256, row_end)); alive && run.next();)
                     delta(run);
+            }
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader, one thread)
@@ -635,9 +644,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_
             for (uint32_t u = c0; u < n_units && alive; u += G, ++t) {
                 base();
                 if constexpr (LORA) {
+                    if (!alive || (u == c0 && !wait(&tab_full, 0)))
+                        break;
                     const int tile0 = row_begin + pair_tile(u, n_pairs, n_ns).pair * 256;
                     Runs run(segs, tile0, min(tile0 + 256, row_end));
-                    if (!alive || !run.next())
+                    if (!run.next())
                         continue;
                     if (!wait(&f_empty, (n_delta & 1) ^ 1))
                         break;
@@ -658,6 +669,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_
         const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + part * kCols;
         unsigned char *const box = sm + kStages * kStage + (warp - 2) * kBox;    // 32 rows
         int t = 0, n_delta = 0;
+        if constexpr (LORA)
+            if (!warp_wait(&tab_full, 0, &abort_flag, p.a.err, p.wait_ns))
+                goto done;
         for (uint32_t u = c0; u < n_units; u += G, ++t) {
             const PairTile un = pair_tile(u, n_pairs, n_ns);
             const int tile0 = row_begin + un.pair * 256;

@@ -58,25 +58,6 @@ __global__ void __launch_bounds__(kVThreads) k_split_shrink(const __grid_constan
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n_stages = p.stages, stage = p.stage;
     const int split = p.split, rank = blockIdx.x % split, tile = blockIdx.x / split;
-    pdl_wait();                                      // the tiles are planned, the workspace is free
-    pdl_trigger();
-    // what ends here ends for the whole cluster: it works on one tile
-    if (tile >= p.hdr->n_groups)
-        return;
-    const Group g = p.groups[tile];
-    const int32_t a = p.seg_ad[g.item];
-    int32_t r = 0;
-    int64_t aoff = 0, boff = 0;
-    if (a == -1)
-        return;
-    if (!pool_adapter_ok(p.pool, a, &r, &aoff, &boff)) {
-        if (tid == 0)
-            atomicOr(p.err, (uint32_t)LORA_ERR_BAD_ADAPTER);
-        return;
-    }
-    const int d_in = p.pool.d_in, n_kb = (d_in + kBK - 1) / kBK, r16 = (r + 15) & ~15;
-    const int k0 = rank * n_kb / split, k1 = (rank + 1) * n_kb / split;
-    const bool view = p.a_tma && aoff % d_in == 0 && aoff / d_in + r <= 0x7fffffffLL;
     int issued = 0;
 
     if (tid == 0) {
@@ -95,6 +76,31 @@ __global__ void __launch_bounds__(kVThreads) k_split_shrink(const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    pdl_wait();                                      // the tiles are planned, the workspace is free
+    pdl_trigger();
+    // what ends here ends for the whole cluster: it works on one tile
+    Group g = {};
+    int32_t a = -1, r = 0;
+    int64_t aoff = 0, boff = 0;
+    if (tile < p.hdr->n_groups) {
+        g = p.groups[tile];
+        a = p.seg_ad[g.item];
+        if (a != -1 && !pool_adapter_ok(p.pool, a, &r, &aoff, &boff)) {
+            if (tid == 0)
+                atomicOr(p.err, (uint32_t)LORA_ERR_BAD_ADAPTER);
+            r = 0;
+        }
+    }
+    if (r == 0) {
+        if (warp == 1)
+            tmem_dealloc(tmem, 128);
+        return;
+    }
+    const int d_in = p.pool.d_in, n_kb = (d_in + kBK - 1) / kBK, r16 = (r + 15) & ~15;
+    const int k0 = rank * n_kb / split, k1 = (rank + 1) * n_kb / split;
+    // (one 64-bit division: 200 instructions, and in the load loop it took longer than a load)
+    const int64_t a_row = aoff / d_in;
+    const bool view = p.a_tma && a_row * d_in == aoff && a_row + r <= 0x7fffffffLL;
 
     if (warp == 0) {
         const uint64_t pol_x = policy_evict_first(), pol_a = policy_evict_last();
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(kVThreads) k_split_shrink(const __grid_constan
                 mbar_arrive_expect_tx(&full_bar[s], kAtom + (view ? r * 128 : 0));
                 tma_load_2d_hint(xs, &p.map_x, &full_bar[s], k * kBK, g.p0, pol_x);
                 if (view) {
-                    const int row = (int)(aoff / d_in);
+                    const int row = (int)a_row;
                     int j = 0;
                     for (; j + 64 <= r; j += 64)
                         tma_load_2d_hint(as + j * 128, &p.map_a[0], &full_bar[s], k * kBK, row + j, pol_a);
