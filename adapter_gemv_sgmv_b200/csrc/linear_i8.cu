@@ -1171,7 +1171,8 @@ template <class T> cudaError_t launch_any(const I8Args &a, cudaStream_t s, bool 
     double best = pair_us(a, n_kb);
     int best_nt = 0, best_split = 1;
     for (int nt : {16, 32, 64, 128, 256}) {
-        if (nt < 128 && nt < a.N)                    // narrow tiles would read the weight again and again
+        // (narrow tiles would read the weight again and again; the model ends at some thousand tokens)
+        if ((nt < 128 && nt < a.N) || a.N > 8192)
             continue;
         for (int split = 1; split <= 8 && (split == 1 || 2 * split <= n_kb); split *= 2) {
             const double us = few_us(a, n_kb, nt, split);

@@ -578,3 +578,49 @@ def test_binding_refuses(bad):
     with pytest.raises(L.LoraError):
         L.lora_linear_i8(Q, Sx, W, Sw, Y)
     assert torch.all(Y == 2)
+
+
+# ------------------------------------------------------------ beyond 32-bit offsets
+def test_outputs_beyond_two_to_the_31_elements():
+    N, d_in, d_out = 150_016, 128, 14_344
+    q = torch.randint(-127, 128, (N, d_in), dtype=torch.int8, device=DEV)
+    w = torch.randint(-127, 128, (d_out, d_in), dtype=torch.int8, device=DEV)
+    Sx, Sw = torch.rand(N, device=DEV), torch.rand(d_out, device=DEV)
+    Y = torch.empty(N, d_out, dtype=torch.bfloat16, device=DEV)
+    ws = L.lora_linear_i8(q, Sx, w, Sw, Y)
+    assert L.lora_get_error(ws) == 0
+    for rows in (slice(0, 300), slice(149_700, N - 20), slice(N - 20, N)):
+        want = (q[rows].double() @ w.double().t()) * Sx[rows].double()[:, None] * Sw.double()
+        tol = want.abs() * (3.001 * 2.0 ** -24 + 2.0 ** -8)
+        assert float(((Y[rows].double() - want).abs() - tol).max()) <= 0
+
+
+def test_quantised_matrix_beyond_two_to_the_31_elements():
+    N, d = 1_100_000, 2048
+    x = torch.empty(N, d, dtype=torch.bfloat16, device=DEV).normal_()
+    Q, S = torch.empty(N, d, dtype=torch.int8, device=DEV), torch.empty(N, device=DEV)
+    L.lora_quant_i8(x, Q, S)
+    for rows in (slice(0, 100), slice(1_048_500, 1_048_700), slice(N - 100, N)):
+        q, s = _quant_ref(x[rows].double().cpu().numpy())
+        assert np.array_equal(Q[rows].cpu().numpy(), q) and np.array_equal(S[rows].cpu().numpy(), s)
+
+
+@pytest.mark.parametrize("rank", [64, 24])
+def test_adapter_stored_beyond_two_to_the_31_elements(rank):
+    """The last adapter of a 4 GB pool of B matrices, through the view of its rank and gathered."""
+    rng = np.random.default_rng(rank)
+    d_in, d_out, N = 128, 264, 300
+    hp = rand_host_pool(rng, [rank], d_in, d_out)
+    X, x, Q, Sx, Wq, Sw, base = _adapted_inputs(rng, N, d_in, d_out)
+    pool = DevPool(hp)
+    far = (1 << 31) + 64 * 24 * 8
+    B = torch.zeros(far + rank * d_out, dtype=torch.bfloat16, device=DEV)
+    B[far:] = pool.B[:rank * d_out]
+    pool.B = B
+    pool.B_off = torch.tensor([far], dtype=torch.int64, device=DEV)
+    off, ads = np.array([0, N], np.int32), np.array([0], np.int32)
+    Y = torch.empty((N, d_out), dtype=torch.bfloat16, device=DEV)
+    ws = L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, pool, _i32(off), _i32(ads), 0.5)
+    assert L.lora_get_error(ws) == 0
+    want = base + oracle.linear_sgmv(X, np.zeros((d_out, d_in), np.uint16), hp, off, ads, 0.5)
+    check_parity(widen(to_host(Y)), want, "far adapter")

@@ -279,3 +279,15 @@ def test_adapted_qkv_with_positions():
         assert float(((v.double() - exact).abs() - tol).max()) <= 0
     v_err = (qkv[:, (heads + kv) * hd:].double() - want[2]).abs() - want[2].abs() * 2.0 ** -8 - 1e-3
     assert float(v_err.max()) <= 0
+
+
+def test_rope_beyond_two_to_the_31_elements():
+    n, h, d = 131_100, 130, 128
+    x = torch.empty(n, h, d, dtype=torch.bfloat16, device=DEV).normal_()
+    ends = [slice(0, 20), slice(n // 2, n // 2 + 20), slice(n - 20, n)]
+    before = [x[e].clone() for e in ends]
+    pos = torch.arange(n, device=DEV)
+    f, _ = _freqs(d)
+    L.lora_rope([x], [x], pos, f)
+    for e, b in zip(ends, before):
+        _check(x[e].clone(), b, pos[e], f, False, 1.0, False, f"rows {e}")
