@@ -395,84 +395,12 @@ def lora_linear_sgmv(X, W, Y, pool, seg_off, seg_ad, scale: float, ws: Workspace
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
 
 
-class _T:
-    """What lora_linear_i8_sgmv looks up in torch on every call, found once."""
-
-    def __init__(self):
-        import torch
-        self.i8, self.i32 = torch.int8, torch.int32
-        self.bf16, self.f32 = torch.bfloat16, torch.float32
-        self.raw_stream = torch._C._cuda_getCurrentRawStream
-        self.current_device = torch._C._cuda_getDevice
-        self.capturing = torch.cuda.is_current_stream_capturing
-        self.device = torch.cuda.device
-        self.stream = torch.cuda.stream
-
-
-_types: _T | None = None
-
-
-def _lib_types():
-    global _types
-    if _types is None:
-        _types = _T()
-    return _lib or load(), _types
-
-
-def _one_device(dev: int, *others: int) -> int:
-    """The tensors' device, given the index of each."""
-    for d in others:
-        if d != dev:
-            dev = -1
-    if dev < 0:
-        raise LoraError("tensors must live on one CUDA device", 1)
-    return dev
-
-
-def _rows(t, name: str, shape):
-    """Leading dimension of a matrix (a single row has none: any that fits will do)."""
-    n, d = shape
-    if t.shape != shape:
-        raise LoraError(f"{name} must be a tensor [{n}, {d}]", 1)
-    ld, unit = t.stride()
-    if unit != 1 and d > 1:
-        raise LoraError(f"{name} must have unit-stride columns", 1)
-    return ld if n > 1 else (d + 15) // 16 * 16
-
-
-def _scales(T, t, n: int, name: str):
-    if t.dtype is not T.f32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
-        raise LoraError(f"{name} must be a contiguous fp32 tensor of {n} scales", 1)
-
-
-_stream_ws: dict = {}
-
-
-def _stream_workspace(T, nbytes: int, dev: int, raw: int, stream):
-    """(workspace, its address, its size) of this device and stream: calls on two streams never
-    share one.  Under graph capture it is a fresh one from the graph's memory, so that no two
-    graphs share it."""
-    if stream is not None and raw != T.raw_stream(dev):
-        with T.stream(stream):                         # allocated, and freed, in that stream's order
-            return _stream_workspace(T, nbytes, dev, raw, None)
-    if T.capturing():
-        return _placed(Workspace(nbytes, device=f"cuda:{dev}"))
-    ws = _stream_ws.get((dev, raw))
-    if ws is None or ws[2] < nbytes:
-        ws = _stream_ws[dev, raw] = _placed(Workspace(max(nbytes, 2 * (ws[2] if ws else 0)), device=f"cuda:{dev}"))
-    return ws
-
-
-def _placed(ws: Workspace):
-    return ws, ws.ptr(), ws.nbytes
-
-
-def _new_workspace(dev: int, stream) -> Workspace:
-    """A header-sized workspace, allocated (and one day freed) in the stream's order."""
+def _new_workspace(dev: int, stream, nbytes: int) -> Workspace:
+    """A workspace allocated (and one day freed) in the stream's order."""
     if stream is None:
-        return Workspace(256, device=f"cuda:{dev}")
+        return Workspace(nbytes, device=f"cuda:{dev}")
     with _torch().cuda.stream(stream):
-        return Workspace(256, device=f"cuda:{dev}")
+        return Workspace(nbytes, device=f"cuda:{dev}")
 
 
 _native_module = None
@@ -491,29 +419,19 @@ def _native():
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
         m.setup(LoraError, _new_workspace, *(ctypes.cast(f, ctypes.c_void_p).value
-                                             for f in (lib.lora_quant_i8, lib.lora_linear_i8, lib.lora_rope)))
+                                             for f in (lib.lora_quant_i8, lib.lora_linear_i8, lib.lora_rope,
+                                                       lib.lora_linear_i8_sgmv, lib.lora_workspace_size)))
         _native_module = m
     return _native_module
 
 
-# Each call below launches on the tensors' device, which need not be the current one.
+# Each call below launches on the tensors' device, which need not be the current one.  Without
+# a ws it uses a workspace of that device and stream (calls on two streams never share one),
+# and under graph capture a fresh one from the graph's memory (nor do two graphs).
 
 def lora_quant_i8(X, Q, S, stream=None):
     """Q[n] = round(127 X[n] / max|X[n]|) (int8), S[n] = max|X[n]| / 127 for rows of bf16, fp16 or fp32."""
     (_native_module or _native()).quant_i8(X, Q, S, stream)
-
-
-def _i8_operands(T, Q, Sx, Wq, Sw, Y):
-    if Q.dtype is not T.i8 or Wq.dtype is not T.i8 or Q.dim() != 2 or Wq.dim() != 2:
-        raise LoraError("Q [N, d_in] and Wq [d_out, d_in] must be int8 matrices", 1)
-    q_shape, w_shape = Q.shape, Wq.shape
-    n, d_in = q_shape
-    d_out, k = w_shape
-    if k != d_in:
-        raise LoraError("Q and Wq disagree on d_in", 1)
-    _scales(T, Sx, n, "Sx")
-    _scales(T, Sw, d_out, "Sw")
-    return n, d_in, d_out, _rows(Q, "Q", q_shape), _rows(Wq, "Wq", w_shape), _rows(Y, "Y", (n, d_out))
 
 
 def lora_linear_i8(Q, Sx, Wq, Sw, Y, ws: Workspace | None = None, stream=None):
@@ -528,35 +446,8 @@ def lora_linear_i8_sgmv(Q, Sx, X, Wq, Sw, Y, pool, seg_off, seg_ad, scale: float
 
     X holds the bf16 tokens that Q and Sx are the 8-bit form of; Y is bf16, overwritten inside
     the segments and left alone outside them."""
-    lib, T = _lib_types()
-    dev = _one_device(*(t.get_device() for t in (Q, Sx, X, Wq, Sw, Y, seg_off, seg_ad, pool.A, pool.B, pool.A_off,
-                                                 pool.B_off, pool.rank)))
-    if T.current_device() != dev:
-        with T.device(dev):
-            return lora_linear_i8_sgmv(Q, Sx, X, Wq, Sw, Y, pool, seg_off, seg_ad, scale, ws, stream, max_rank)
-    n, d_in, d_out, ldq, ldw, ldy = _i8_operands(T, Q, Sx, Wq, Sw, Y)
-    ps = make_pool_struct(pool, max_rank)
-    ldx = _rows(X, "X", (n, d_in))
-    if X.dtype is not T.bf16 or Y.dtype is not T.bf16:
-        raise LoraError("X and Y must be bf16", 1)
-    if d_in != ps.d_in or d_out != ps.d_out:
-        raise LoraError("Wq must be [pool.d_out, pool.d_in]", 1)
-    n_seg = seg_ad.numel()
-    for t, need, name in ((seg_off, n_seg + 1, "seg_off"), (seg_ad, n_seg, "seg_ad")):
-        if t.dtype is not T.i32 or t.numel() < need or not t.is_contiguous():
-            raise LoraError(f"{name} must be a contiguous int32 tensor of {need} entries", 1)
-    raw = T.raw_stream(dev) if stream is None else stream.cuda_stream
-    if ws is None:
-        need = lib.lora_workspace_size(OP_LINEAR_I8_SGMV, n, ps.n_adapters, d_in, d_out, ps.max_rank, n_seg, 1)
-        ws, at, size = _stream_workspace(T, need, dev, raw, stream)
-    else:
-        ws, at, size = _placed(ws)
-    rc = lib.lora_linear_i8_sgmv(Q.data_ptr(), ldq, Sx.data_ptr(), X.data_ptr(), ldx, Wq.data_ptr(), ldw,
-                                 Sw.data_ptr(), Y.data_ptr(), ldy, ctypes.byref(ps), seg_off.data_ptr(),
-                                 seg_ad.data_ptr(), n_seg, n, float(scale), at, size, raw)
-    if rc:
-        raise LoraError("lora_linear_i8_sgmv", rc)
-    return ws
+    return (_native_module or _native()).linear_i8_sgmv(Q, Sx, X, Wq, Sw, Y, pool, seg_off, seg_ad, scale, ws, stream,
+                                                        max_rank)
 
 
 def lora_rope(xs, ys, pos, freqs, interleaved: bool = False, mscale: float = 1.0, inverse: bool = False,

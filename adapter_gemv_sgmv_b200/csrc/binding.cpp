@@ -1,9 +1,9 @@
-// Native marshalling of the calls that a decode step makes eagerly, one after another:
-// lora_quant_i8, lora_linear_i8, lora_rope.  Their kernels take 2 to 10 us; reading the
-// arguments' attributes from Python and converting them with ctypes took 6 to 9 us a call,
-// the launch itself 2.5.  This file checks the same things on the tensors' C++ side and
-// calls the same C ABI (its entry points are handed in, so the library is loaded in one
-// place only).
+// Native marshalling of the calls that a decode step or a short prompt makes eagerly, one
+// after another: lora_quant_i8, lora_linear_i8, lora_linear_i8_sgmv, lora_rope.  Their
+// kernels take 2 to 20 us; reading the arguments' attributes from Python and converting them
+// with ctypes took 6 to 9 us a call (22 with a pool: 9 here), one launch 2.5.  This file checks
+// the same things on the tensors' C++ side and calls the same C ABI (its entry points are
+// handed in, so the library is loaded in one place only).
 
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <map>
 #include <utility>
 
@@ -21,20 +22,22 @@
 namespace {
 
 PyObject *g_error = nullptr;            // LoraError(what, code)
-PyObject *g_new_workspace = nullptr;    // (device, stream or None) -> Workspace
+PyObject *g_new_workspace = nullptr;    // (device, stream or None, bytes) -> Workspace
 decltype(&lora_quant_i8) g_quant = nullptr;
 decltype(&lora_linear_i8) g_linear = nullptr;
 decltype(&lora_rope) g_rope = nullptr;
+decltype(&lora_linear_i8_sgmv) g_sgmv = nullptr;
+decltype(&lora_workspace_size) g_workspace_size = nullptr;
 
 struct Refused {                        // thrown inside a call, raised as LoraError at its end
     const char *what;
     int code;
 };
 
-struct Workspace {                      // the workspace of a device and stream, kept for good
-    PyObject *object;
-    void *at;
-    size_t bytes;
+struct Workspace {                      // the workspace of a device and stream, kept until a larger one is needed
+    PyObject *object = nullptr;
+    void *at = nullptr;
+    size_t bytes = 0;
 };
 std::map<std::pair<int, cudaStream_t>, Workspace> g_workspaces;
 
@@ -87,8 +90,8 @@ int32_t dtype(const at::Tensor &t)
 
 int32_t as_i32(int64_t v)
 {
-    if (v > 0x7fffffffLL)
-        throw Refused{"more than 2^31 - 1 rows or columns", LORA_ERR_UNSUPPORTED};
+    if (v != (int32_t)v)
+        throw Refused{"sizes must fit 32 bits", LORA_ERR_UNSUPPORTED};
     return (int32_t)v;
 }
 
@@ -110,7 +113,8 @@ cudaStream_t stream_of(PyObject *o, int dev)
 Workspace read_workspace(PyObject *o)
 {
     PyObject *at = PyObject_CallMethod(o, "ptr", nullptr), *n = at ? PyObject_GetAttrString(o, "nbytes") : nullptr;
-    Workspace w = {o, nullptr, 0};
+    Workspace w;
+    w.object = o;
     if (at && n) {
         w.at = PyLong_AsVoidPtr(at);
         w.bytes = PyLong_AsSize_t(n);
@@ -124,7 +128,7 @@ Workspace read_workspace(PyObject *o)
 
 // A new reference to the call's workspace: the one given, else this device and stream's;
 // under graph capture a fresh one from the graph's memory, so that no two graphs share it.
-Workspace workspace(PyObject *given, PyObject *stream, int dev, cudaStream_t s)
+Workspace workspace(PyObject *given, PyObject *stream, int dev, cudaStream_t s, size_t bytes)
 {
     if (given != Py_None) {
         Workspace w = read_workspace(given);
@@ -140,11 +144,14 @@ Workspace workspace(PyObject *given, PyObject *stream, int dev, cudaStream_t s)
     if (capturing == cudaStreamCaptureStatusNone) {
         const auto it = g_workspaces.find(key);
         if (it != g_workspaces.end()) {
-            Py_INCREF(it->second.object);
-            return it->second;
+            if (it->second.bytes >= bytes) {
+                Py_INCREF(it->second.object);
+                return it->second;
+            }
+            bytes = std::max(bytes, 2 * it->second.bytes);
         }
     }
-    PyObject *o = PyObject_CallFunction(g_new_workspace, "iO", dev, stream);
+    PyObject *o = PyObject_CallFunction(g_new_workspace, "iOn", dev, stream, (Py_ssize_t)bytes);
     if (!o)
         throw std::exception();
     Workspace w;
@@ -156,7 +163,10 @@ Workspace workspace(PyObject *given, PyObject *stream, int dev, cudaStream_t s)
     }
     if (capturing == cudaStreamCaptureStatusNone) {
         Py_INCREF(o);
-        g_workspaces[key] = w;
+        Workspace &kept = g_workspaces[key];
+        PyObject *old = kept.object;
+        kept = w;
+        Py_XDECREF(old);
     }
     return w;
 }
@@ -223,37 +233,170 @@ PyObject *quant_i8(PyObject *, PyObject *const *a, Py_ssize_t n_args)
     });
 }
 
+// The operands of a projection with an 8-bit weight.
+struct I8 {
+    int dev;
+    int64_t ldq, ldw, ldy;
+    const int8_t *q, *w;
+    const float *sx, *sw;
+    void *y;
+    int32_t type, n, d_in, d_out;
+
+    I8(PyObject *oq, PyObject *osx, PyObject *ow, PyObject *osw, PyObject *oy)
+    {
+        const at::Tensor &Q = tensor(oq, "Q must be a tensor"), &Sx = tensor(osx, "Sx must be a tensor"),
+                         &W = tensor(ow, "Wq must be a tensor"), &Sw = tensor(osw, "Sw must be a tensor"),
+                         &Y = tensor(oy, "Y must be a tensor");
+        dev = device_of(Y, device_of(Sw, device_of(W, device_of(Sx, device_of(Q, -1)))));
+        if (Q.scalar_type() != at::kChar || W.scalar_type() != at::kChar || Q.dim() != 2 || W.dim() != 2 ||
+            Q.size(1) != W.size(1))
+            throw Refused{"Q [N, d_in] and Wq [d_out, d_in] must be int8 matrices", LORA_ERR_INVALID_ARG};
+        n = as_i32(Q.size(0));
+        d_in = as_i32(Q.size(1));
+        d_out = as_i32(W.size(0));
+        ldq = rows(Q, n, d_in, "Q must have unit-stride columns");
+        ldw = rows(W, d_out, d_in, "Wq must have unit-stride columns");
+        ldy = rows(Y, n, d_out, "Y must be [N, d_out] with unit-stride columns");
+        sx = scales(Sx, n, "Sx must be a contiguous fp32 tensor, one scale a token");
+        sw = scales(Sw, d_out, "Sw must be a contiguous fp32 tensor, one scale a channel");
+        q = static_cast<const int8_t *>(Q.data_ptr());
+        w = static_cast<const int8_t *>(W.data_ptr());
+        y = Y.data_ptr();
+        type = dtype(Y);
+    }
+};
+
 // linear_i8(Q, Sx, Wq, Sw, Y, workspace or None, stream) -> workspace
 PyObject *linear_i8(PyObject *, PyObject *const *a, Py_ssize_t n_args)
 {
     if (!takes(n_args, 7))
         return nullptr;
     return guarded([&]() -> PyObject * {
-        const at::Tensor &Q = tensor(a[0], "Q must be a tensor"), &Sx = tensor(a[1], "Sx must be a tensor"),
-                         &W = tensor(a[2], "Wq must be a tensor"), &Sw = tensor(a[3], "Sw must be a tensor"),
-                         &Y = tensor(a[4], "Y must be a tensor");
-        const int dev = device_of(Y, device_of(Sw, device_of(W, device_of(Sx, device_of(Q, -1)))));
-        if (Q.scalar_type() != at::kChar || W.scalar_type() != at::kChar || Q.dim() != 2 || W.dim() != 2 ||
-            Q.size(1) != W.size(1))
-            throw Refused{"Q [N, d_in] and Wq [d_out, d_in] must be int8 matrices", LORA_ERR_INVALID_ARG};
-        const int64_t n = Q.size(0), d_in = Q.size(1), d_out = W.size(0);
-        const int64_t ldq = rows(Q, n, d_in, "Q must have unit-stride columns");
-        const int64_t ldw = rows(W, d_out, d_in, "Wq must have unit-stride columns");
-        const int64_t ldy = rows(Y, n, d_out, "Y must be [N, d_out] with unit-stride columns");
-        const float *sx = scales(Sx, n, "Sx must be a contiguous fp32 tensor, one scale a token");
-        const float *sw = scales(Sw, d_out, "Sw must be a contiguous fp32 tensor, one scale a channel");
-        const int32_t t = dtype(Y), n32 = as_i32(n), i32 = as_i32(d_in), o32 = as_i32(d_out);
+        const I8 o(a[0], a[1], a[2], a[3], a[4]);
         c10::cuda::OptionalCUDAGuard guard;
-        if (c10::cuda::current_device() != dev)
-            guard.set_index(dev);
-        const cudaStream_t s = stream_of(a[6], dev);
-        const Workspace ws = workspace(a[5], a[6], dev, s);
-        const int rc = g_linear(static_cast<const int8_t *>(Q.data_ptr()), ldq, sx,
-                                static_cast<const int8_t *>(W.data_ptr()), ldw, sw, Y.data_ptr(), t, ldy, n32, i32, o32,
-                                ws.at, ws.bytes, s);
+        if (c10::cuda::current_device() != o.dev)
+            guard.set_index(o.dev);
+        const cudaStream_t s = stream_of(a[6], o.dev);
+        const Workspace ws = workspace(a[5], a[6], o.dev, s, 256);
+        const int rc = g_linear(o.q, o.ldq, o.sx, o.w, o.ldw, o.sw, o.y, o.type, o.ldy, o.n, o.d_in, o.d_out, ws.at,
+                                ws.bytes, s);
         if (rc != LORA_OK) {
             Py_DECREF(ws.object);
             return raise("lora_linear_i8", rc);
+        }
+        return ws.object;
+    });
+}
+
+// A pool object's tensors and sizes (the attributes hold the references).
+struct Pool {
+    PyObject *held[5] = {};
+    lora_pool p = {};
+
+    Pool(PyObject *o, PyObject *max_rank, int dev)
+    {
+        static const char *const names[5] = {"A", "B", "A_off", "B_off", "rank"};
+        static const char *const wrong[5] = {"pool.A must be contiguous bf16", "pool.B must be contiguous bf16",
+                                             "pool.A_off must be contiguous int64", "pool.B_off must be contiguous int64",
+                                             "pool.rank must be contiguous int32"};
+        const at::ScalarType types[5] = {at::kBFloat16, at::kBFloat16, at::kLong, at::kLong, at::kInt};
+        const void *ptr[5];
+        int64_t n[5];
+        try {
+            for (int i = 0; i < 5; ++i) {
+                if (!(held[i] = PyObject_GetAttrString(o, names[i])))
+                    throw std::exception();
+                const at::Tensor &t = tensor(held[i], wrong[i]);
+                device_of(t, dev);
+                if (t.scalar_type() != types[i] || !t.is_contiguous())
+                    throw Refused{wrong[i], LORA_ERR_INVALID_ARG};
+                ptr[i] = t.data_ptr();
+                n[i] = t.numel();
+            }
+            p.A = ptr[0];
+            p.B = ptr[1];
+            p.A_off = static_cast<const int64_t *>(ptr[2]);
+            p.B_off = static_cast<const int64_t *>(ptr[3]);
+            p.rank = static_cast<const int32_t *>(ptr[4]);
+            p.A_elems = n[0];
+            p.B_elems = n[1];
+            if (n[2] < n[4] || n[3] < n[4])
+                throw Refused{"pool.A_off and pool.B_off need an entry for every rank", LORA_ERR_INVALID_ARG};
+            p.n_adapters = as_i32(n[4]);
+            p.d_in = size(o, "d_in");
+            p.d_out = size(o, "d_out");
+            p.max_rank = max_rank == Py_None ? size(o, "max_rank") : as_i32(PyLong_AsLongLong(max_rank));
+            if (PyErr_Occurred())
+                throw std::exception();
+        } catch (...) {
+            drop();
+            throw;
+        }
+    }
+    ~Pool() { drop(); }
+    Pool(const Pool &) = delete;
+
+private:
+    static int32_t size(PyObject *o, const char *name)
+    {
+        PyObject *v = PyObject_GetAttrString(o, name);
+        if (!v)
+            throw std::exception();
+        const long long x = PyLong_AsLongLong(v);
+        Py_DECREF(v);
+        if (PyErr_Occurred())
+            throw std::exception();
+        return as_i32(x);
+    }
+    void drop()
+    {
+        for (PyObject *&h : held)
+            Py_CLEAR(h);
+    }
+};
+
+const int32_t *ints(const at::Tensor &t, int64_t least, const char *what)
+{
+    if (t.scalar_type() != at::kInt || t.numel() < least || !t.is_contiguous())
+        throw Refused{what, LORA_ERR_INVALID_ARG};
+    return static_cast<const int32_t *>(t.data_ptr());
+}
+
+// linear_i8_sgmv(Q, Sx, X, Wq, Sw, Y, pool, seg_off, seg_ad, scale, workspace or None, stream, max_rank or None)
+PyObject *linear_i8_sgmv(PyObject *, PyObject *const *a, Py_ssize_t n_args)
+{
+    if (!takes(n_args, 13))
+        return nullptr;
+    return guarded([&]() -> PyObject * {
+        const I8 o(a[0], a[1], a[3], a[4], a[5]);
+        const at::Tensor &X = tensor(a[2], "X must be a tensor"), &off = tensor(a[7], "seg_off must be a tensor"),
+                         &ad = tensor(a[8], "seg_ad must be a tensor");
+        device_of(ad, device_of(off, device_of(X, o.dev)));
+        if (X.scalar_type() != at::kBFloat16 || o.type != LORA_BF16)
+            throw Refused{"X and Y must be bf16", LORA_ERR_INVALID_ARG};
+        const int64_t ldx = rows(X, o.n, o.d_in, "X must be [N, d_in] with unit-stride columns");
+        const Pool pool(a[6], a[12], o.dev);
+        if (pool.p.d_in != o.d_in || pool.p.d_out != o.d_out)
+            throw Refused{"Wq must be [pool.d_out, pool.d_in]", LORA_ERR_INVALID_ARG};
+        const int32_t n_seg = as_i32(ad.numel());
+        const int32_t *seg_ad = ints(ad, n_seg, "seg_ad must be a contiguous int32 tensor");
+        const int32_t *seg_off = ints(off, (int64_t)n_seg + 1, "seg_off must be a contiguous int32 tensor of n_seg + 1");
+        const double scale = PyFloat_AsDouble(a[9]);
+        if (PyErr_Occurred())
+            throw std::exception();
+        c10::cuda::OptionalCUDAGuard guard;
+        if (c10::cuda::current_device() != o.dev)
+            guard.set_index(o.dev);
+        const cudaStream_t s = stream_of(a[11], o.dev);
+        // (sizes the call refuses need none)
+        const size_t need = g_workspace_size(LORA_OP_LINEAR_I8_SGMV, o.n, pool.p.n_adapters, o.d_in, o.d_out,
+                                             pool.p.max_rank, n_seg, 1);
+        const Workspace ws = workspace(a[10], a[11], o.dev, s, std::max<size_t>(need, 256));
+        const int rc = g_sgmv(o.q, o.ldq, o.sx, X.data_ptr(), ldx, o.w, o.ldw, o.sw, o.y, o.ldy, &pool.p, seg_off, seg_ad,
+                              n_seg, o.n, (float)scale, ws.at, ws.bytes, s);
+        if (rc != LORA_OK) {
+            Py_DECREF(ws.object);
+            return raise("lora_linear_i8_sgmv", rc);
         }
         return ws.object;
     });
@@ -320,13 +463,14 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n_args)
     return done;
 }
 
-// setup(LoraError, new_workspace, addresses of lora_quant_i8, lora_linear_i8 and lora_rope)
+// setup(LoraError, new_workspace, addresses of lora_quant_i8, lora_linear_i8, lora_rope,
+// lora_linear_i8_sgmv and lora_workspace_size)
 PyObject *setup(PyObject *, PyObject *const *a, Py_ssize_t n_args)
 {
-    if (!takes(n_args, 5))
+    if (!takes(n_args, 7))
         return nullptr;
-    void *f[3];
-    for (int i = 0; i < 3; ++i)
+    void *f[5];
+    for (int i = 0; i < 5; ++i)
         f[i] = PyLong_AsVoidPtr(a[2 + i]);
     if (PyErr_Occurred())
         return nullptr;
@@ -337,6 +481,8 @@ PyObject *setup(PyObject *, PyObject *const *a, Py_ssize_t n_args)
     g_quant = reinterpret_cast<decltype(g_quant)>(f[0]);
     g_linear = reinterpret_cast<decltype(g_linear)>(f[1]);
     g_rope = reinterpret_cast<decltype(g_rope)>(f[2]);
+    g_sgmv = reinterpret_cast<decltype(g_sgmv)>(f[3]);
+    g_workspace_size = reinterpret_cast<decltype(g_workspace_size)>(f[4]);
     Py_RETURN_NONE;
 }
 
@@ -344,6 +490,7 @@ PyObject *setup(PyObject *, PyObject *const *a, Py_ssize_t n_args)
 PyMethodDef g_methods[] = {{"setup", FAST(setup), nullptr},
                            {"quant_i8", FAST(quant_i8), nullptr},
                            {"linear_i8", FAST(linear_i8), nullptr},
+                           {"linear_i8_sgmv", FAST(linear_i8_sgmv), nullptr},
                            {"rope", FAST(rope), nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

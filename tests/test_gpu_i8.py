@@ -624,3 +624,66 @@ def test_adapter_stored_beyond_two_to_the_31_elements(rank):
     assert L.lora_get_error(ws) == 0
     want = base + oracle.linear_sgmv(X, np.zeros((d_out, d_in), np.uint16), hp, off, ads, 0.5)
     check_parity(widen(to_host(Y)), want, "far adapter")
+
+
+def test_adapted_workspace_grows_between_calls():
+    """On a new stream, a small call, a larger one behind it and the small one again, nothing
+    waited for: the larger workspace takes the place of the one still in use."""
+    rng = np.random.default_rng(41)
+    d_in, d_out = 520, 264
+    hp = rand_host_pool(rng, [8, 64, 128], d_in, d_out)
+    pool = DevPool(hp)
+    jobs = []
+    for lens, ads in (([3, 4], [0, 1]), ([900, 700, 600], [2, 1, 0]), ([3, 4], [1, 2])):
+        off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+        X, x, Q, Sx, Wq, Sw, base = _adapted_inputs(rng, int(off[-1]), d_in, d_out)
+        want = base + oracle.linear_sgmv(X, np.zeros((d_out, d_in), np.uint16), hp, off, np.array(ads, np.int32), 1.5)
+        Y = torch.zeros((int(off[-1]), d_out), dtype=torch.bfloat16, device=DEV)
+        jobs.append((Q, Sx, x, Wq, Sw, Y, pool, _i32(off), _i32(ads), 1.5, want))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    used = [L.lora_linear_i8_sgmv(*job[:-1], stream=s) for job in jobs]
+    s.synchronize()
+    assert used[1] is used[2] and used[1].nbytes >= used[0].nbytes
+    for job, ws in zip(jobs, used):
+        assert L.lora_get_error(ws) == 0
+        check_parity(widen(to_host(job[5])), job[-1], "grown workspace")
+
+
+@pytest.mark.parametrize("bad", ["x type", "y type", "x shape", "pool width", "pool type", "pool host", "pool table",
+                                 "seg_off", "seg_ad type", "rank", "missing"])
+def test_adapted_binding_refuses(bad):
+    rng = np.random.default_rng(43)
+    hp = rand_host_pool(rng, [8, 16], 64, 32)
+    X, x, Q, Sx, Wq, Sw, base = _adapted_inputs(rng, 20, 64, 32)
+    pool = DevPool(hp)
+    a = dict(Q=Q, Sx=Sx, X=x, Wq=Wq, Sw=Sw, Y=torch.zeros((20, 32), dtype=torch.bfloat16, device=DEV), pool=pool,
+             seg_off=_i32([0, 10, 20]), seg_ad=_i32([0, 1]), scale=1.0)
+    error = L.LoraError
+    if bad == "x type":
+        a["X"] = x.half()
+    elif bad == "y type":
+        a["Y"] = a["Y"].float()
+    elif bad == "x shape":
+        a["X"] = x[:19]
+    elif bad == "pool width":
+        pool.d_out = 40
+    elif bad == "pool type":
+        pool.A_off = pool.A_off.int()
+    elif bad == "pool host":
+        pool.B = pool.B.cpu()
+    elif bad == "pool table":
+        pool.B_off = pool.B_off[:1]
+    elif bad == "seg_off":
+        a["seg_off"] = a["seg_off"][:2]
+    elif bad == "seg_ad type":
+        a["seg_ad"] = a["seg_ad"].long()
+    elif bad == "rank":
+        a["max_rank"] = 2**33
+    else:
+        a["pool"], error = object(), AttributeError
+    before = a["Y"].clone()
+    with pytest.raises(error):
+        L.lora_linear_i8_sgmv(**a)
+    torch.cuda.synchronize()
+    assert torch.equal(a["Y"], before)
