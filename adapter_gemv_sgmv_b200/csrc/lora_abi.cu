@@ -827,20 +827,25 @@ lora_status lora_linear_i8_sgmv(const int8_t *Q, int64_t ldq, const float *Sx, c
     Group *groups = at<Group>(ws, L.groups);
 
     // tiles, then s V as bf16 high and low parts
-    PlanArgs pa = {};
-    pa.mode = kModeSgmv;
-    pa.N = N;
-    pa.item_off = seg_off;
-    pa.n_items = n_seg;
-    pa.groups = groups;
-    pa.max_groups = L.max_groups;
-    pa.group = kTcGroup;
-    pa.hdr = hdr;
-    LORA_CUDA(launch_plan(pa, s));
     SplitShrinkArgs va = {};
-    va.groups = groups;
+    if (n_seg > kSplitShrinkSegs) {
+        PlanArgs pa = {};
+        pa.mode = kModeSgmv;
+        pa.N = N;
+        pa.item_off = seg_off;
+        pa.n_items = n_seg;
+        pa.groups = groups;
+        pa.max_groups = L.max_groups;
+        pa.group = kTcGroup;
+        pa.hdr = hdr;
+        LORA_CUDA(launch_plan(pa, s));
+        va.groups = groups;
+    }
     va.hdr = hdr;
+    va.seg_off = seg_off;
     va.seg_ad = seg_ad;
+    va.n_seg = n_seg;
+    va.N = N;
     va.pool = pool_dev(pool);
     va.scale = scale;
     va.Vb = at<__nv_bfloat16>(ws, L.V);

@@ -343,9 +343,11 @@ struct SplitShrinkArgs {
     int32_t a_tma;           // the A maps are valid
     int32_t split;           // CTAs that share a tile's reduction (this and the next two: set by the launcher)
     int32_t stage, stages;   // bytes of a ring stage, stages
-    const Group *groups;     // tiles of <= 128 rows, one segment each
-    const WsHeader *hdr;
+    const Group *groups;     // tiles of <= 128 rows, one segment each; null: the kernel finds them itself
+    WsHeader *hdr;           // (and leaves n_groups and the error bit as the plan kernel does)
+    const int32_t *seg_off;
     const int32_t *seg_ad;   // -1: no adapter
+    int32_t n_seg, N;
     PoolDev pool;
     float scale;
     __nv_bfloat16 *Vb;       // scale * v: high part at Vb[n][c], low part at Vb[n][vb_lo + c]
@@ -355,6 +357,7 @@ struct SplitShrinkArgs {
     unsigned long long wait_ns;   // bound of every wait (set by the launcher)
     int32_t test_stall;           // the producer issues nothing (set by the launcher)
 };
+constexpr int kSplitShrinkSegs = 128;   // segments up to which it finds its tiles itself
 cudaError_t launch_split_shrink(const SplitShrinkArgs &a, const void *X, int64_t ldx, int32_t N, int max_tiles,
                                 cudaStream_t s, bool *ok);
 

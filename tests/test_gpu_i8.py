@@ -687,3 +687,48 @@ def test_adapted_binding_refuses(bad):
         L.lora_linear_i8_sgmv(**a)
     torch.cuda.synchronize()
     assert torch.equal(a["Y"], before)
+
+
+@pytest.mark.parametrize("n_seg", [1, 2, 5, 31, 33, 125, 127, 128, 129, 160])
+def test_adapted_segment_counts(n_seg):
+    """Segments of every length class (none, one row, a tile to the row, tiles and a rest), on both
+    sides of the count up to which the shrink finds its tiles itself."""
+    rng = np.random.default_rng(100 + n_seg)
+    d_in, d_out = 1032, 136
+    hp = rand_host_pool(rng, [8, 64, 128, 32, 16, 40], d_in, d_out)
+    lens = rng.choice([0, 1, 2, 7, 20, 127, 128, 129, 256, 300], n_seg, p=[.2, .2, .2, .1, .1, .04, .04, .04, .04, .04])
+    lens[n_seg // 2] = 385
+    _run_adapted(rng, hp, lens, rng.integers(-1, 6, n_seg).astype(np.int32), d_in, d_out, 0.5, start=3, tail=2,
+                 what=f"adapted, {n_seg} segments of mixed lengths")
+
+
+@pytest.mark.parametrize("n_seg", [4, 128, 140])
+@pytest.mark.parametrize("bad", ["falls", "negative", "behind the last row", "far", "all negative"])
+def test_adapted_bad_offsets_leave_the_output(n_seg, bad):
+    rng = np.random.default_rng(45)
+    N = 2 * n_seg
+    hp = rand_host_pool(rng, [16, 32], 64, 32)
+    X, x, Q, Sx, Wq, Sw, base = _adapted_inputs(rng, N, 64, 32)
+    off = 2 * np.arange(n_seg + 1, dtype=np.int64)
+    if bad == "falls":
+        off[n_seg - 2] = off[n_seg - 3] - 1
+    elif bad == "negative":
+        off[0] = -1
+    elif bad == "behind the last row":
+        off[n_seg] = N + 1
+    elif bad == "far":
+        off[n_seg - 1] = 2**31 - 1
+    else:
+        off[:] = -5
+    Y = torch.ones((N, 32), dtype=torch.bfloat16, device=DEV)
+    args = Q, Sx, x, Wq, Sw, Y, DevPool(hp)
+    ads = _i32(np.arange(n_seg) % 2)
+    ws = L.lora_linear_i8_sgmv(*args, _i32(off), ads, 1.0)
+    assert L.lora_get_error(ws) == 8
+    assert torch.all(Y == 1)
+    good = _i32(2 * np.arange(n_seg + 1))
+    L.lora_linear_i8_sgmv(*args, good, ads, 1.0, ws=ws)       # and the workspace is fit for the next call
+    assert L.lora_get_error(ws) == 0
+    want = base + oracle.linear_sgmv(X, np.zeros((32, 64), np.uint16), hp, 2 * np.arange(n_seg + 1, dtype=np.int32),
+                                     (np.arange(n_seg) % 2).astype(np.int32), 1.0)
+    check_parity(widen(to_host(Y)), want, "after bad offsets")
