@@ -832,7 +832,29 @@ done:
 // come from the kernel before (which quantises the tokens), so their lines are requested
 // into L2 ahead of the wait for it -- a prefetch only: the loads follow the wait, for that
 // kernel may have written this very weight.
+//
+// With adapters (LORA) the base does not wait for the shrink in front of it: what that kernel
+// waited for is all the base reads, so the product runs beside it, and only the finish waits
+// for V.  There the cluster's tokens are cut into groups of eight; a warp adds to 8 tokens x
+// 32 outputs the delta of each adapter among them, by mma.sync in registers (the adapter's B
+// rows and the tokens' V straight from L2; columns of other adapters' tokens are not taken
+// over, so that an infinity in B stays with its own tokens).  The delta is a few MFLOP: a
+// tcgen05 product would need B in shared memory and a TMEM round trip for it.
 constexpr int kFewThreads = 192;         // producer, MMA issuer, 4 warps that empty the accumulator
+
+struct __align__(16) FewTok {            // a token's adapter
+    int64_t boff;
+    int32_t a;
+    int32_t r;                           // rank; 0: no delta, -1: outside the segments
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
 template <int NT> struct FewCfg {
     static constexpr int stage = kAtom + NT * 128;
@@ -872,7 +894,142 @@ __device__ __forceinline__ int ld_remote(uint32_t addr)
     return v;
 }
 
-template <int NT, class T>
+// The adapter of each of the tile's tokens, by the four warps that empty the accumulator.
+__device__ void few_tokens(const I8Args &a, FewTok *tok, int n0, int nv, int t0)
+{
+    for (int t = t0; t < nv; t += 128)
+        tok[t] = {0, -1, -1};
+    __syncwarp();
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    for (int k = t0; k < a.n_seg; k += 128) {        // (bad offsets mark anything: nothing is written then)
+        const int lo = max(__ldcg(a.seg_off + k), n0) - n0, hi = min(__ldcg(a.seg_off + k + 1), n0 + nv) - n0;
+        for (int t = lo; t < hi; ++t)
+            tok[t].a = k;
+    }
+    __syncwarp();
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    for (int t = t0; t < nv; t += 128)
+        if (tok[t].a >= 0) {
+            const int32_t ad = __ldcg(a.seg_ad + tok[t].a);
+            int32_t r = 0;
+            int64_t ao = 0, bo = 0;
+            // (the shrink reports a bad one)
+            if (ad == -1 || !pool_adapter_ok(a.pool, ad, &r, &ao, &bo))
+                tok[t] = {0, -1, 0};
+            else
+                tok[t] = {bo, ad, r};
+        }
+}
+
+// B rows o .. o + 3 at ranks k .. k + 7 and k + 32 .. k + 39 (zeros behind the last).
+__device__ __forceinline__ void few_load_b(const I8Args &p, const FewTok &ad, int o, int k, uint4 (&b)[2][4])
+{
+    const __nv_bfloat16 *b_row = p.pool.B + ad.boff + (int64_t)o * ad.r + k;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            b[h][i] = make_uint4(0, 0, 0, 0);
+            if (o < p.d_out && k + 32 * h < ad.r)
+                b[h][i] = __ldcg(reinterpret_cast<const uint4 *>(b_row + i * ad.r + 32 * h));
+        }
+}
+
+// Finishes 8 tokens t .. of the tile x 32 outputs from `ob`: the base from the cluster's sums
+// at `part`, and the deltas.  The MMA's rows and reduction are numbered so that a thread has
+// four outputs in a row (o ..) of two tokens (t + 2q, t + 2q + 1) and loads eight ranks at
+// once: rows g, g + 8 of the first product are outputs 4g, 4g + 1, of the second 4g + 2,
+// 4g + 3, and columns 2q, 2q + 1, 2q + 8, 2q + 9 of a pair of steps are ranks 8q .. 8q + 7.
+// All but V is fetched before the wait for the shrink.
+__device__ __forceinline__ void few_finish(const I8Args &p, const FewTok *tok, uint32_t part, int split, int n0, int t,
+                                           int t_end, int ob, int lane)
+{
+    const int g = lane >> 2, q = lane & 3, o = ob + 4 * g;
+    const bool o_ok = o < p.d_out;
+    const bool tok_ok = lane < 8 && t + lane < t_end && tok[min(t + lane, t_end - 1)].r > 0;
+    const int my_ad = tok[min(t + (lane & 7), t_end - 1)].a;
+    uint32_t left = __ballot_sync(0xffffffffu, tok_ok);
+    uint4 b[2][4];
+    if (left)
+        few_load_b(p, tok[t + __ffs(left) - 1], o, 8 * q, b);
+    float y[4][2] = {};
+    if (o_ok) {
+        const float sw[4] = {p.Sw[o], p.Sw[o + 1], p.Sw[o + 2], p.Sw[o + 3]};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (t + 2 * q + j < t_end) {
+                const float sx = p.Sx[n0 + t + 2 * q + j];
+                int4 v[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (c < split)
+                        v[c] = ld_remote_v4(map_rank(part + (t + 2 * q + j) * 512 + (o & 127) * 4, c));
+                int4 a = v[0];
+#pragma unroll
+                for (int c = 1; c < 8; ++c)
+                    if (c < split) {
+                        a.x += v[c].x;
+                        a.y += v[c].y;
+                        a.z += v[c].z;
+                        a.w += v[c].w;
+                    }
+                y[0][j] = (float)a.x * (sx * sw[0]);
+                y[1][j] = (float)a.y * (sx * sw[1]);
+                y[2][j] = (float)a.z * (sx * sw[2]);
+                y[3][j] = (float)a.w * (sx * sw[3]);
+            }
+    }
+    pdl_wait();
+    const bool write = __ldcg(&p.hdr->n_groups) != 0;
+    const __nv_bfloat16 *v_row = p.Vb + (int64_t)(n0 + min(t + g, t_end - 1)) * p.ldvb + 8 * q;
+    bool have_b = true;
+    while (left) {
+        const FewTok ad = tok[t + __ffs(left) - 1];
+        const uint32_t same = __ballot_sync(0xffffffffu, tok_ok && my_ad == ad.a);
+        left &= ~same;
+        float d0[4] = {}, d1[4] = {};
+        for (int k = 0; k < ad.r; k += 64) {
+            uint4 vh[2] = {}, vl[2] = {};
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (k + 32 * h + 8 * q < ad.r) {
+                    vh[h] = __ldcg(reinterpret_cast<const uint4 *>(v_row + k + 32 * h));
+                    vl[h] = __ldcg(reinterpret_cast<const uint4 *>(v_row + p.kv + k + 32 * h));
+                }
+            if (!have_b)
+                few_load_b(p, ad, o, k + 8 * q, b);
+            have_b = false;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mma_bf16(d0, b[h][0].x, b[h][1].x, b[h][0].y, b[h][1].y, vh[h].x, vh[h].y);
+                mma_bf16(d1, b[h][2].x, b[h][3].x, b[h][2].y, b[h][3].y, vh[h].x, vh[h].y);
+                mma_bf16(d0, b[h][0].z, b[h][1].z, b[h][0].w, b[h][1].w, vh[h].z, vh[h].w);
+                mma_bf16(d1, b[h][2].z, b[h][3].z, b[h][2].w, b[h][3].w, vh[h].z, vh[h].w);
+                mma_bf16(d0, b[h][0].x, b[h][1].x, b[h][0].y, b[h][1].y, vl[h].x, vl[h].y);
+                mma_bf16(d1, b[h][2].x, b[h][3].x, b[h][2].y, b[h][3].y, vl[h].x, vl[h].y);
+                mma_bf16(d0, b[h][0].z, b[h][1].z, b[h][0].w, b[h][1].w, vl[h].z, vl[h].w);
+                mma_bf16(d1, b[h][2].z, b[h][3].z, b[h][2].w, b[h][3].w, vl[h].z, vl[h].w);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if ((same >> (2 * q + j)) & 1) {
+                y[0][j] += d0[j];
+                y[1][j] += d0[2 + j];
+                y[2][j] += d1[j];
+                y[3][j] += d1[2 + j];
+            }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int tj = t + 2 * q + j;
+        if (o_ok && write && tj < t_end && tok[tj].r >= 0)
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.Y) + (int64_t)(n0 + tj) * p.ldy + o) =
+                make_uint2(pack2(y[0][j], y[1][j], __nv_bfloat16()), pack2(y[2][j], y[3][j], __nv_bfloat16()));
+    }
+}
+
+template <int NT, class T, bool LORA>
 __global__ void __launch_bounds__(kFewThreads) k_i8_few(const __grid_constant__ FewTc p)
 {
     using C = FewCfg<NT>;
@@ -883,6 +1040,7 @@ __global__ void __launch_bounds__(kFewThreads) k_i8_few(const __grid_constant__ 
     __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], acc_full, mma_drain;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
+    __shared__ FewTok tok[LORA ? NT : 1];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int split = p.split, rank = (int)cluster_rank();
@@ -910,12 +1068,15 @@ __global__ void __launch_bounds__(kFewThreads) k_i8_few(const __grid_constant__ 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
-    pdl_wait();
+    if constexpr (!LORA)
+        pdl_wait();
     pdl_trigger();
 
     if (warp == 0) {
         if (lane == 0 && !p.test_stall) {
             const uint64_t pol_x = policy_evict_last(), pol_w = policy_evict_first();
+            if constexpr (LORA)                      // (written by a kernel that no wait here names)
+                asm volatile("fence.proxy.async;" ::: "memory");
             for (int k = k0; k < k1; ++k, ++issued) {
                 const int s = issued % kStages;
                 if (!mbar_wait(&empty_bar[s], ((issued / kStages) & 1) ^ 1, &abort_flag, p.a.err, p.wait_ns))
@@ -952,6 +1113,8 @@ __global__ void __launch_bounds__(kFewThreads) k_i8_few(const __grid_constant__ 
     } else {
         // partial sums to shared memory as [token][128 outputs], in the ring's place: every
         // fill has been multiplied when the accumulator is full
+        if constexpr (LORA)
+            few_tokens(p.a, tok, n0, nv, tid - 64);
         const int q = warp & 3;
         if (warp_wait(&acc_full, 0, &abort_flag, p.a.err, p.wait_ns)) {
             tc_fence_after();
@@ -986,7 +1149,15 @@ __global__ void __launch_bounds__(kFewThreads) k_i8_few(const __grid_constant__ 
         whole &= ld_remote(map_rank(smem_u32(&abort_flag), r)) == 0;
     const int per = (nv + split - 1) / split;
     const int o = o0 + lane * 4;
-    if (whole && o < p.a.d_out) {
+    if constexpr (LORA) {
+        const int t_end = min(nv, (rank + 1) * per);
+        if (whole)
+            for (int u = warp; rank * per + (u >> 2) * 8 < t_end; u += kFewThreads / 32)
+                if (o0 + (u & 3) * 32 < p.a.d_out)
+                    few_finish(p.a, tok, smem_u32(sm), split, n0, rank * per + (u >> 2) * 8, t_end, o0 + (u & 3) * 32, lane);
+        pdl_wait();                                  // (who had nothing to finish, too: this kernel's
+                                                     // end stands for the shrink's)
+    } else if (whole && o < p.a.d_out) {
         const uint32_t mine = smem_u32(sm) + lane * 16;
         float sw[4];
 #pragma unroll
@@ -1099,7 +1270,7 @@ template <class C, class T> cudaError_t launch_pair(const I8Args &a, cudaStream_
     return cudaLaunchKernelEx(&cfg, k_i8_pair<C, T>, p);
 }
 
-template <int NT, class T> cudaError_t launch_few(const I8Args &a, int split, cudaStream_t s, bool *ok)
+template <int NT, class T, bool LORA> cudaError_t launch_few(const I8Args &a, int split, cudaStream_t s, bool *ok)
 {
     using C = FewCfg<NT>;
     FewTc p = {};
@@ -1116,7 +1287,7 @@ template <int NT, class T> cudaError_t launch_few(const I8Args &a, int split, cu
     if (e != cudaSuccess)
         return e;
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        if ((e = cudaFuncSetAttribute(k_i8_few<NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem)) != cudaSuccess)
+        if ((e = cudaFuncSetAttribute(k_i8_few<NT, T, LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem)) != cudaSuccess)
             return e;
         if (dev >= 0 && dev < 64)
             attr_set[dev] = true;
@@ -1135,7 +1306,7 @@ template <int NT, class T> cudaError_t launch_few(const I8Args &a, int split, cu
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k_i8_few<NT, T>, p);
+    return cudaLaunchKernelEx(&cfg, k_i8_few<NT, T, LORA>, p);
 }
 
 // Microseconds of a call without adapters, by a model fitted to B200 timings over N = 1 ..
@@ -1165,40 +1336,97 @@ double few_us(const I8Args &a, int n_kb, int nt, int split)
     return (nt <= 64 ? 5.5 : (nt <= 128 ? 6.5 : 8.1)) + load * kb * (16384 + nt * 128) / 85e3;
 }
 
-template <class T> cudaError_t launch_any(const I8Args &a, cudaStream_t s, bool *ok)
+// The same with adapters, the shrink in front included (about 4.5 and d_in / 850).
+// * CTA pairs start behind it, and every tile adds its epilogue and each run of rows with one
+//   adapter: 1.5 a run, 2.5 with ranks over 64, less from the seventh on; two thirds of it in
+//   tiles of 128 outputs.
+// * Few tokens multiply beside it where the CTAs of both find room, then finish in rounds of
+//   six warps: 1.1 a round, and 0.9 (ranks over 64: 1.1) for each adapter among eight tokens.
+// Measured (us, pairs / few): 16 tokens in 4 segments, 4096 -> 4096 29.6 / 14.0, 14336 -> 4096
+// 65 / 23.5; 256 in 8, 4096 -> 4096 36.7 / 25.7; 512 in 8 35.9 / 35.5; 1024 in 16 41.6 / 61,
+// 4096 -> 1024 35.8 / 26.1; 256 in 8, 4096 -> 14336 44 / 54.
+double shrink_us(const I8Args &a)
 {
-    const int n_kb = (a.d_in + kKB - 1) / kKB;
-    double best = pair_us(a, n_kb);
-    int best_nt = 0, best_split = 1;
+    return 4.5 + a.d_in / 850.0;
+}
+
+bool narrow_pairs(const I8Args &a)
+{
+    return ((int64_t)a.N + 255) / 256 * ((a.d_out + 127) / 128) <= sm_count() / 2;
+}
+
+double pair_lora_us(const I8Args &a, int n_kb)
+{
+    double runs = 1 + 256.0 * a.n_seg / a.N;
+    if (runs > a.n_seg)
+        runs = a.n_seg;
+    const double first = a.pool.max_rank <= 64 ? 1.5 : 2.5, more = a.pool.max_rank <= 64 ? 0.6 : 1.0;
+    const double tile = 3 + (runs < 6 ? runs * first : 6 * first + (runs - 6) * more);
+    const int64_t tiles = ((int64_t)a.N + 255) / 256 * ((a.d_out + 255) / 256);
+    return shrink_us(a) + 2.5 + pair_us(a, n_kb) + (narrow_pairs(a) ? 0.65 * tile : (double)((tiles + 73) / 74) * tile);
+}
+
+double few_lora_us(const I8Args &a, int n_kb, int nt, int split)
+{
+    const int64_t ctas = (int64_t)((a.d_out + 127) / 128) * (((int64_t)a.N + nt - 1) / nt) * split;
+    const int tokens = nt < a.N ? nt : a.N, groups = ((tokens + split - 1) / split + 7) / 8;
+    const double runs = 1 + 8.0 * a.n_seg / a.N;
+    const double finish = 2 + (groups * 4 + 5) / 6 * (1.1 + (a.pool.max_rank <= 64 ? 0.9 : 1.1) * (runs < 8 ? runs : 8));
+    const double base = few_us(a, n_kb, nt, split), shrink = shrink_us(a);
+    // (the shrink splits a tile over up to 8 CTAs of 8 of its k-blocks)
+    const int64_t before = ((int64_t)a.N / 128 + a.n_seg) * (n_kb < 8 ? 1 : (n_kb < 32 ? n_kb / 4 : 8));
+    if (ctas <= 240 && ctas + before <= 296)
+        return (base > shrink ? base : shrink) + finish;
+    return 0.75 * shrink + base + (double)((ctas + 239) / 240) * finish;
+}
+
+// The few-token form that a model expects to be fastest, and its time.
+struct FewChoice {
+    int nt, split;
+    double us;
+};
+
+FewChoice best_few(const I8Args &a, int n_kb, int max_nt, double (*model)(const I8Args &, int, int, int))
+{
+    FewChoice best = {0, 1, 1e30};
     for (int nt : {16, 32, 64, 128, 256}) {
         // (narrow tiles would read the weight again and again; the model ends at some thousand tokens)
-        if ((nt < 128 && nt < a.N) || a.N > 8192)
+        if ((nt < 128 && nt < a.N) || nt > max_nt || a.N > 8192)
             continue;
         for (int split = 1; split <= 8 && (split == 1 || 2 * split <= n_kb); split *= 2) {
-            const double us = few_us(a, n_kb, nt, split);
-            if (us < best) {
-                best = us;
-                best_nt = nt;
-                best_split = split;
-            }
+            const double us = model(a, n_kb, nt, split);
+            if (us < best.us)
+                best = {nt, split, us};
         }
         if (nt >= a.N)
             break;
     }
-    switch (best_nt) {
+    return best;
+}
+
+template <class T, bool LORA> cudaError_t launch_few_nt(const I8Args &a, const FewChoice &c, cudaStream_t s, bool *ok)
+{
+    switch (c.nt) {
     case 16:
-        return launch_few<16, T>(a, best_split, s, ok);
+        return launch_few<16, T, LORA>(a, c.split, s, ok);
     case 32:
-        return launch_few<32, T>(a, best_split, s, ok);
+        return launch_few<32, T, LORA>(a, c.split, s, ok);
     case 64:
-        return launch_few<64, T>(a, best_split, s, ok);
-    case 128:
-        return launch_few<128, T>(a, best_split, s, ok);
+        return launch_few<64, T, LORA>(a, c.split, s, ok);
     case 256:
-        return launch_few<256, T>(a, best_split, s, ok);
+        if constexpr (!LORA)
+            return launch_few<256, T, false>(a, c.split, s, ok);
     default:
-        return launch_pair<PairCfg<false, 256>, T>(a, s, ok);
+        return launch_few<128, T, LORA>(a, c.split, s, ok);
     }
+}
+
+template <class T> cudaError_t launch_any(const I8Args &a, cudaStream_t s, bool *ok)
+{
+    const int n_kb = (a.d_in + kKB - 1) / kKB;
+    const FewChoice few = best_few(a, n_kb, 256, few_us);
+    return few.us < pair_us(a, n_kb) ? launch_few_nt<T, false>(a, few, s, ok)
+                                     : launch_pair<PairCfg<false, 256>, T>(a, s, ok);
 }
 
 }  // namespace
@@ -1206,11 +1434,15 @@ template <class T> cudaError_t launch_any(const I8Args &a, cudaStream_t s, bool 
 cudaError_t launch_linear_i8(const I8Args &a, cudaStream_t s, bool *ok)
 {
     if (a.seg_off) {
+        const int n_kb = (a.d_in + kKB - 1) / kKB;
+        // (256 tokens a CTA were never faster than 128: twice the finishing of one CTA)
+        const FewChoice few = best_few(a, n_kb, 128, few_lora_us);
+        if (few.us < pair_lora_us(a, n_kb))
+            return launch_few_nt<__nv_bfloat16, true>(a, few, s, ok);
         // Tiles of 128 outputs where they still find a free pair of SMs each: the gathers and
         // the emptying of a tile halve (1535 tokens in 23 segments, 4096 -> 1024: 52 against 57 us
         // for the whole call), its loads do not.
-        const int64_t pairs = ((int64_t)a.N + 255) / 256;
-        if (pairs * ((a.d_out + 127) / 128) <= sm_count() / 2)
+        if (narrow_pairs(a))
             return launch_pair<PairCfg<true, 128>, __nv_bfloat16>(a, s, ok);
         return launch_pair<PairCfg<true, 256>, __nv_bfloat16>(a, s, ok);
     }

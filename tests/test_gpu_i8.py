@@ -732,3 +732,80 @@ def test_adapted_bad_offsets_leave_the_output(n_seg, bad):
     want = base + oracle.linear_sgmv(X, np.zeros((32, 64), np.uint16), hp, 2 * np.arange(n_seg + 1, dtype=np.int32),
                                      (np.arange(n_seg) % 2).astype(np.int32), 1.0)
     check_parity(widen(to_host(Y)), want, "after bad offsets")
+
+
+@pytest.mark.parametrize("N", [16, 24, 100, 256, 1000])
+def test_adapted_operands_written_right_before(N):
+    """Tokens, weight, adapters and segments that the kernels just before the call wrote: each
+    round brings other ones, and nothing waits in between."""
+    rng = np.random.default_rng(51)
+    d_in, d_out, rounds = 2048, 1032, 5
+    hps = [rand_host_pool(rng, [64, 24], d_in, d_out) for _ in range(rounds)]
+    pools = [DevPool(h) for h in hps]
+    pool = DevPool(hps[0])
+    X = [rand_x(rng, N, d_in) for _ in range(rounds)]
+    xs = [dev_bf16(a) for a in X]
+    Ws = [torch.randn(d_out, d_in, device=DEV) / d_in ** 0.5 for _ in range(rounds)]
+    offs = [np.array([0, c, N], np.int32) for c in rng.integers(1, N, rounds)]
+    offs_dev = [_i32(o) for o in offs]
+    x, W, off = torch.empty_like(xs[0]), torch.empty_like(Ws[0]), torch.empty_like(offs_dev[0])
+    Q, Sx = torch.empty(N, d_in, dtype=torch.int8, device=DEV), torch.empty(N, device=DEV)
+    Wq, Sw = torch.empty(d_out, d_in, dtype=torch.int8, device=DEV), torch.empty(d_out, device=DEV)
+    Ys = [torch.zeros(N, d_out, dtype=torch.bfloat16, device=DEV) for _ in range(rounds)]
+    ads = _i32([1, 0])
+    wants = []
+    for i in range(rounds):
+        L.lora_quant_i8(xs[i], Q, Sx)
+        L.lora_quant_i8(Ws[i], Wq, Sw)
+        base = (Q.double() @ Wq.double().t()) * Sx.double()[:, None] * Sw.double()
+        wants.append(base.cpu().numpy() + oracle.linear_sgmv(X[i], np.zeros((d_out, d_in), np.uint16), hps[i], offs[i],
+                                                             np.array([1, 0], np.int32), 0.5))
+    torch.cuda.synchronize()
+    for i in range(rounds):
+        off.copy_(offs_dev[i])
+        pool.A.copy_(pools[i].A)
+        pool.B.copy_(pools[i].B)
+        x.copy_(xs[i])
+        L.lora_quant_i8(Ws[i], Wq, Sw)
+        L.lora_quant_i8(x, Q, Sx)
+        L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Ys[i], pool, off, ads, 0.5)
+    torch.cuda.synchronize()
+    for Y, want in zip(Ys, wants):
+        check_parity(widen(to_host(Y)), want, "operands written right before")
+        check_rounded(widen(to_host(Y)), want, "operands written right before")
+
+
+@pytest.mark.parametrize("d_in,d_out", [(8, 8), (136, 40), (2048, 264), (14336, 136)])
+@pytest.mark.parametrize("lens", [[1], [1, 1, 1], [0, 7, 0, 1], [8, 8], [3, 17, 5, 9], [30, 1, 40, 2], [100, 28],
+                                  [65, 64, 1, 126], [1] * 37, [200, 313]])
+def test_adapted_few_tokens(lens, d_in, d_out):
+    """Few tokens, where adapters change inside a group of eight and ranks end inside 32."""
+    rng = np.random.default_rng(sum(lens) + d_in)
+    hp = rand_host_pool(rng, [8, 64, 24, 128, 40], d_in, d_out)
+    ads = rng.integers(-1, 5, len(lens)).astype(np.int32)
+    ads[0] = len(lens) % 5
+    _run_adapted(rng, hp, lens, ads, d_in, d_out, 0.5, start=0 if len(lens) < 4 else 3, tail=len(lens) % 3,
+                 what="adapted, few tokens")
+
+
+@pytest.mark.parametrize("N", [24, 1200])
+def test_adapted_infinity_stays_with_its_own_tokens(N):
+    """An adapter with an infinite B row and a NaN beside another's tokens, and beside tokens
+    without any: theirs are finite and right."""
+    rng = np.random.default_rng(53)
+    d_in, d_out = 256, 72
+    hp = rand_host_pool(rng, [16, 32], d_in, d_out)
+    pool = DevPool(hp)
+    pool.B[int(hp.B_off[1]):] = float("inf")
+    pool.B[int(hp.B_off[1]) + 5] = float("nan")
+    off = np.array([0, 3, 6, 9, 14, N], np.int32)
+    ads = np.array([0, 1, -1, 1, 0], np.int32)
+    X, x, Q, Sx, Wq, Sw, base = _adapted_inputs(rng, N, d_in, d_out)
+    Y = torch.zeros((N, d_out), dtype=torch.bfloat16, device=DEV)
+    L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, pool, _i32(off), _i32(ads), 0.5)
+    want = base + oracle.linear_sgmv(X, np.zeros((d_out, d_in), np.uint16), hp, off,
+                                     np.where(ads == 1, -1, ads).astype(np.int32), 0.5)
+    rows = np.r_[0:3, 6:9, 14:N]
+    got = widen(to_host(Y))
+    check_parity(got[rows], want[rows], "beside infinities")
+    assert not np.isfinite(got[np.r_[3:6, 9:14]]).any()
