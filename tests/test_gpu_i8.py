@@ -809,3 +809,117 @@ def test_adapted_infinity_stays_with_its_own_tokens(N):
     got = widen(to_host(Y))
     check_parity(got[rows], want[rows], "beside infinities")
     assert not np.isfinite(got[np.r_[3:6, 9:14]]).any()
+
+
+# Behind 8192 rows the CTA pairs always run, below some hundred the few-token kernel does: what
+# the tests above check at one size is checked for the other kernel here.
+PAIRS = 8193
+
+
+@pytest.mark.parametrize("d_in,d_out", [(8, 8), (328, 200), (256, 520), (136, 264), (1032, 72)])
+def test_adapted_pairs_ragged(d_in, d_out):
+    rng = np.random.default_rng(d_in * 11 + d_out)
+    hp = rand_host_pool(rng, [16, 32, 128, 64, 24], d_in, d_out)
+    lens = [130, 1, 255, 0, 128, 37, 300, 64, 3, 1, 0, 2, 700]
+    ads = [2, 0, 4, 1, 3, -1, 1, 2, 3, 3, 1, 0, 4, -1]
+    _run_adapted(rng, hp, lens + [PAIRS - sum(lens)], ads, d_in, d_out, 0.75, what=f"pairs {d_in}x{d_out}")
+
+
+@pytest.mark.parametrize("scatter", [False, True])
+@pytest.mark.parametrize("N", [200, PAIRS])
+def test_adapted_any_rank_both_kernels(N, scatter):
+    rng = np.random.default_rng(5 + scatter)
+    d_in, d_out = 192, 648
+    hp = rand_host_pool(rng, [8, 24, 40, 16, 96, 64, 120, 128], d_in, d_out)
+    if scatter:
+        hp = scatter_pool(hp)
+    cuts = np.sort(rng.integers(0, N, 15))
+    _run_adapted(rng, hp, np.diff(np.r_[0, cuts, N]), np.arange(16, dtype=np.int32) % 8, d_in, d_out, 1.5,
+                 what=f"any rank, {N} rows, scatter={scatter}")
+
+
+@pytest.mark.parametrize("n_seg", [127, 128, 129, 511, 512, 513, 700])
+@pytest.mark.parametrize("N", [150, PAIRS])
+def test_adapted_hundreds_of_segments_both_kernels(N, n_seg):
+    rng = np.random.default_rng(n_seg + N)
+    d_in, d_out = 128, 264
+    hp = rand_host_pool(rng, [8, 64, 128, 32, 16, 40], d_in, d_out)
+    cuts = np.sort(rng.integers(0, N + 1, n_seg - 1))
+    _run_adapted(rng, hp, np.diff(np.r_[0, cuts, N]), rng.integers(-1, 6, n_seg).astype(np.int32), d_in, d_out, 0.5,
+                 what=f"{n_seg} segments in {N} rows")
+
+
+@pytest.mark.parametrize("N", [7, 40, PAIRS])
+def test_adapted_times_out_and_recovers_both_kernels(N):
+    rng = np.random.default_rng(47)
+    d_in, d_out = 1024, 264
+    hp = rand_host_pool(rng, [32, 64], d_in, d_out)
+    off, ads = np.array([0, N // 2, N], np.int32), np.array([1, 0], np.int32)
+    X, x, Q, Sx, Wq, Sw, base = _adapted_inputs(rng, N, d_in, d_out)
+    pool = DevPool(hp)
+    Y = torch.ones((N, d_out), dtype=torch.bfloat16, device=DEV)
+    assert _stalled(lambda: L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, pool, _i32(off), _i32(ads), 0.5)) & 64
+    assert torch.all(Y == 1)
+    ws = L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, pool, _i32(off), _i32(ads), 0.5)
+    assert L.lora_get_error(ws) == 0
+    want = base + oracle.linear_sgmv(X, np.zeros((d_out, d_in), np.uint16), hp, off, ads, 0.5)
+    check_parity(widen(to_host(Y)), want, "adapted after a timeout")
+
+
+@pytest.mark.parametrize("N", [9, PAIRS])
+def test_adapted_bad_metadata_both_kernels(N):
+    """A bad adapter's rows get the base alone; a bad offset leaves every row."""
+    rng = np.random.default_rng(48)
+    d_in, d_out = 128, 136
+    hp = rand_host_pool(rng, [16, 32], d_in, d_out)
+    X, x, Q, Sx, Wq, Sw, base = _adapted_inputs(rng, N, d_in, d_out)
+    pool = DevPool(hp)
+    off, ads = np.array([0, 4, N], np.int32), np.array([7, 0], np.int32)
+    Y = torch.ones((N, d_out), dtype=torch.bfloat16, device=DEV)
+    ws = L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, pool, _i32(off), _i32(ads), 1.0)
+    assert L.lora_get_error(ws) == 4
+    want = base + oracle.linear_sgmv(X, np.zeros((d_out, d_in), np.uint16), hp, off, np.array([-1, 0], np.int32), 1.0)
+    check_parity(widen(to_host(Y)), want, "bad adapter")
+    for wrong in ([0, N, N - 1], [0, 4, N + 1], [-1, 4, N]):
+        Y.fill_(1.0)
+        ws = L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, pool, _i32(wrong), _i32([1, 0]), 1.0)
+        assert L.lora_get_error(ws) == 8
+        assert torch.all(Y == 1)
+
+
+@pytest.mark.parametrize("N", [20, 130])
+def test_adapted_few_tokens_captured_and_on_two_streams(N):
+    """Two captured chains of the few-token form replay side by side on new inputs."""
+    rng = np.random.default_rng(49)
+    d_in, d_out = 2048, 520
+    hp = rand_host_pool(rng, [64, 40], d_in, d_out)
+    pool = DevPool(hp)
+    off, ads = np.array([0, N // 3, N], np.int32), np.array([1, 0], np.int32)
+    jobs = []
+    for _ in range(2):
+        sets = [_adapted_inputs(rng, N, d_in, d_out) for _ in range(3)]
+        x, Wq, Sw = sets[0][1].clone(), sets[0][4], sets[0][5]
+        Q, Sx = torch.empty(N, d_in, dtype=torch.int8, device=DEV), torch.empty(N, device=DEV)
+        Y = torch.zeros(N, d_out, dtype=torch.bfloat16, device=DEV)
+        seg_off, seg_ad = _i32(off), _i32(ads)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(3):
+                L.lora_quant_i8(x, Q, Sx)
+                L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, pool, seg_off, seg_ad, 0.5)
+        jobs.append((g, x, Q, Sx, Wq, Sw, Y, sets, torch.cuda.Stream(), (seg_off, seg_ad)))
+    for i in range(3):
+        for g, x, Q, Sx, Wq, Sw, Y, sets, s, _ in jobs:
+            x.copy_(sets[i][1])
+            Y.zero_()
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for job in jobs:
+                with torch.cuda.stream(job[8]):
+                    job[0].replay()
+        torch.cuda.synchronize()
+        for g, x, Q, Sx, Wq, Sw, Y, sets, s, _ in jobs:
+            base = ((Q.double() @ Wq.double().t()) * Sx.double()[:, None] * Sw.double()).cpu().numpy()
+            want = base + oracle.linear_sgmv(sets[i][0], np.zeros((d_out, d_in), np.uint16), hp, off, ads, 0.5)
+            check_parity(widen(to_host(Y)), want, "replayed few tokens")
