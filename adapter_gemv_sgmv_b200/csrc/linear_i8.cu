@@ -1371,13 +1371,13 @@ double few_lora_us(const I8Args &a, int n_kb, int nt, int split)
     const int64_t ctas = (int64_t)((a.d_out + 127) / 128) * (((int64_t)a.N + nt - 1) / nt) * split;
     const int tokens = nt < a.N ? nt : a.N, groups = ((tokens + split - 1) / split + 7) / 8;
     const double runs = 1 + 8.0 * a.n_seg / a.N;
-    const double finish = 2 + (groups * 4 + 5) / 6 * (1.1 + (a.pool.max_rank <= 64 ? 0.9 : 1.1) * (runs < 8 ? runs : 8));
+    const double finish = 0.5 + (groups * 4 + 5) / 6 * (1.1 + (a.pool.max_rank <= 64 ? 0.9 : 1.1) * (runs < 8 ? runs : 8));
     const double base = few_us(a, n_kb, nt, split), shrink = shrink_us(a);
     // (the shrink splits a tile over up to 8 CTAs of 8 of its k-blocks)
     const int64_t before = ((int64_t)a.N / 128 + a.n_seg) * (n_kb < 8 ? 1 : (n_kb < 32 ? n_kb / 4 : 8));
     if (ctas <= 240 && ctas + before <= 296)
-        return (base > shrink ? base : shrink) + finish;
-    return 0.75 * shrink + base + (double)((ctas + 239) / 240) * finish;
+        return (base > shrink ? base + 0.25 * shrink : shrink + 0.25 * base) + finish;
+    return 0.75 * shrink + base + (double)((ctas + 239) / 240) * (1.5 + finish);
 }
 
 // The few-token form that a model expects to be fastest, and its time.

@@ -339,7 +339,7 @@ struct I8Args {
 // s V of the segments' tiles as bf16 high and low parts (shrink_split.cu)
 struct SplitShrinkArgs {
     CUtensorMap map_x;       // X [N, d_in], boxes 64 x 128, 128-byte swizzle (this and the next: set by the launcher)
-    CUtensorMap map_a[3];    // A pool as [A_elems / d_in, d_in], boxes of 64 columns x 64 / 32 / 8 rows
+    CUtensorMap map_a[5];    // A pool as [A_elems / d_in, d_in], boxes of 64 columns x 128 / 64 / 32 / 16 / 8 rows
     int32_t a_tma;           // the A maps are valid
     int32_t split;           // CTAs that share a tile's reduction (this and the next two: set by the launcher)
     int32_t stage, stages;   // bytes of a ring stage, stages

@@ -183,14 +183,16 @@ __global__ void __launch_bounds__(kVThreads) k_split_shrink(const __grid_constan
                 mbar_arrive_expect_tx(&full_bar[s], kAtom + (view ? r * 128 : 0));
                 tma_load_2d_hint(xs, &p.map_x, &full_bar[s], k * kBK, g.p0, pol_x);
                 if (view) {
+                    // a box for every binary digit of the rank (each costs 60 ns a k-block: 24 loads
+                    // of 8 rows more took 1.7 us of 21 at d_in 14336)
                     const int row = (int)a_row;
                     int j = 0;
-                    for (; j + 64 <= r; j += 64)
-                        tma_load_2d_hint(as + j * 128, &p.map_a[0], &full_bar[s], k * kBK, row + j, pol_a);
-                    for (; j + 32 <= r; j += 32)
-                        tma_load_2d_hint(as + j * 128, &p.map_a[1], &full_bar[s], k * kBK, row + j, pol_a);
-                    for (; j < r; j += 8)
-                        tma_load_2d_hint(as + j * 128, &p.map_a[2], &full_bar[s], k * kBK, row + j, pol_a);
+#pragma unroll
+                    for (int m = 0; m < 5; ++m)
+                        if (r & (128 >> m)) {
+                            tma_load_2d_hint(as + j * 128, &p.map_a[m], &full_bar[s], k * kBK, row + j, pol_a);
+                            j += 128 >> m;
+                        }
                 }
             }
             __syncwarp();
@@ -310,10 +312,10 @@ cudaError_t launch_split_shrink(const SplitShrinkArgs &a_in, const void *X, int6
     if (!*ok)
         return cudaSuccess;
     const int64_t rows = a.pool.A_elems / d_in;
-    const int boxes[3] = {64, 32, 8};
     a.a_tma = rows >= 1 && rows <= 0x7fffffffLL;
-    for (int m = 0; m < 3 && a.a_tma; ++m)
-        a.a_tma = encode_box(&a.map_a[m], a.pool.A, rows, d_in, d_in, boxes[m]);
+    for (int m = 0; m < 5 && a.a_tma; ++m)
+        a.a_tma = 128 >> m > a.pool.max_rank ||
+                  encode_box(&a.map_a[m], a.pool.A, rows, d_in, d_in, 128 >> m);
     // as many CTAs as two to an SM hold at once, each with eight k-blocks at least
     const int n_kb = (d_in + kBK - 1) / kBK;
     a.split = 1;
