@@ -1336,18 +1336,18 @@ double few_us(const I8Args &a, int n_kb, int nt, int split)
     return (nt <= 64 ? 5.5 : (nt <= 128 ? 6.5 : 8.1)) + load * kb * (16384 + nt * 128) / 85e3;
 }
 
-// The same with adapters, the shrink in front included (about 4.5 and d_in / 850).
+// The same with adapters, the shrink in front included (about 6 and d_in / 1500).
 // * CTA pairs start behind it, and every tile adds its epilogue and each run of rows with one
 //   adapter: 1.5 a run, 2.5 with ranks over 64, less from the seventh on; two thirds of it in
 //   tiles of 128 outputs.
 // * Few tokens multiply beside it where the CTAs of both find room, then finish in rounds of
 //   six warps: 1.1 a round, and 0.9 (ranks over 64: 1.1) for each adapter among eight tokens.
-// Measured (us, pairs / few): 16 tokens in 4 segments, 4096 -> 4096 29.6 / 14.0, 14336 -> 4096
-// 65 / 23.5; 256 in 8, 4096 -> 4096 36.7 / 25.7; 512 in 8 35.9 / 35.5; 1024 in 16 41.6 / 61,
+// Measured (us, pairs / few): 16 tokens in 4 segments, 4096 -> 4096 29 / 13.0, 14336 -> 4096
+// 62 / 20.4; 256 in 8, 4096 -> 4096 36.7 / 25.7; 512 in 8 35.9 / 35.5; 1024 in 16 41.6 / 61,
 // 4096 -> 1024 35.8 / 26.1; 256 in 8, 4096 -> 14336 44 / 54.
 double shrink_us(const I8Args &a)
 {
-    return 4.5 + a.d_in / 850.0;
+    return 6 + a.d_in / 1500.0;
 }
 
 bool narrow_pairs(const I8Args &a)
