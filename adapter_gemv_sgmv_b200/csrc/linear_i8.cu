@@ -841,6 +841,7 @@ done:
 // over, so that an infinity in B stays with its own tokens).  The delta is a few MFLOP: a
 // tcgen05 product would need B in shared memory and a TMEM round trip for it.
 constexpr int kFewThreads = 192;         // producer, MMA issuer, 4 warps that empty the accumulator
+constexpr int kFewLoraThreads = 256;     // and two more for the finish (two CTAs of 128 registers a thread fill an SM)
 
 struct __align__(16) FewTok {            // a token's adapter
     int64_t boff;
@@ -1030,7 +1031,7 @@ __device__ __forceinline__ void few_finish(const I8Args &p, const FewTok *tok, u
 }
 
 template <int NT, class T, bool LORA>
-__global__ void __launch_bounds__(kFewThreads) k_i8_few(const __grid_constant__ FewTc p)
+__global__ void __launch_bounds__(LORA ? kFewLoraThreads : kFewThreads) k_i8_few(const __grid_constant__ FewTc p)
 {
     using C = FewCfg<NT>;
     constexpr int kStages = C::stages, kCols = NT < 32 ? 32 : NT;
@@ -1110,7 +1111,7 @@ __global__ void __launch_bounds__(kFewThreads) k_i8_few(const __grid_constant__ 
             if (ok)
                 tc_commit(&acc_full);
         }
-    } else {
+    } else if (warp < 6) {
         // partial sums to shared memory as [token][128 outputs], in the ring's place: every
         // fill has been multiplied when the accumulator is full
         if constexpr (LORA)
@@ -1152,7 +1153,7 @@ __global__ void __launch_bounds__(kFewThreads) k_i8_few(const __grid_constant__ 
     if constexpr (LORA) {
         const int t_end = min(nv, (rank + 1) * per);
         if (whole)
-            for (int u = warp; rank * per + (u >> 2) * 8 < t_end; u += kFewThreads / 32)
+            for (int u = warp; rank * per + (u >> 2) * 8 < t_end; u += kFewLoraThreads / 32)
                 if (o0 + (u & 3) * 32 < p.a.d_out)
                     few_finish(p.a, tok, smem_u32(sm), split, n0, rank * per + (u >> 2) * 8, t_end, o0 + (u & 3) * 32, lane);
         pdl_wait();                                  // (who had nothing to finish, too: this kernel's
@@ -1301,7 +1302,7 @@ template <int NT, class T, bool LORA> cudaError_t launch_few(const I8Args &a, in
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.d_out + 127) / 128 * split, (a.N + NT - 1) / NT);
-    cfg.blockDim = dim3(kFewThreads);
+    cfg.blockDim = dim3(LORA ? kFewLoraThreads : kFewThreads);
     cfg.dynamicSmemBytes = C::smem;
     cfg.stream = s;
     cfg.attrs = attr;
@@ -1341,10 +1342,11 @@ double few_us(const I8Args &a, int n_kb, int nt, int split)
 //   adapter: 1.5 a run, 2.5 with ranks over 64, less from the seventh on; two thirds of it in
 //   tiles of 128 outputs.
 // * Few tokens multiply beside it where the CTAs of both find room, then finish in rounds of
-//   six warps: 1.1 a round, and 0.9 (ranks over 64: 1.1) for each adapter among eight tokens.
+//   eight warps: 1.1 a round, and 0.9 (ranks over 64: 1.1) for each adapter among eight tokens.
 // Measured (us, pairs / few): 16 tokens in 4 segments, 4096 -> 4096 29 / 13.0, 14336 -> 4096
-// 62 / 20.4; 256 in 8, 4096 -> 4096 36.7 / 25.7; 512 in 8 35.9 / 35.5; 1024 in 16 41.6 / 61,
-// 4096 -> 1024 35.8 / 26.1; 256 in 8, 4096 -> 14336 44 / 54.
+// 62 / 20.4; 256 in 16, 4096 -> 4096 38 / 24.0; 1024 in 16, 4096 -> 1024 34.4 / 23.4; 560 in
+// 10, 8496 -> 6632 79 / 103; 1706 in 24, 3336 -> 3560 74 / 110.  Over 112 random shapes of 16
+// to 2900 tokens the choice takes 2 % longer than the better of all.
 double shrink_us(const I8Args &a)
 {
     return 6 + a.d_in / 1500.0;
@@ -1371,13 +1373,14 @@ double few_lora_us(const I8Args &a, int n_kb, int nt, int split)
     const int64_t ctas = (int64_t)((a.d_out + 127) / 128) * (((int64_t)a.N + nt - 1) / nt) * split;
     const int tokens = nt < a.N ? nt : a.N, groups = ((tokens + split - 1) / split + 7) / 8;
     const double runs = 1 + 8.0 * a.n_seg / a.N;
-    const double finish = 0.5 + (groups * 4 + 5) / 6 * (1.1 + (a.pool.max_rank <= 64 ? 0.9 : 1.1) * (runs < 8 ? runs : 8));
+    const double finish = 2 + (groups * 4 + 7) / 8 * (1.1 + (a.pool.max_rank <= 64 ? 0.9 : 1.1) * (runs < 8 ? runs : 8));
     const double base = few_us(a, n_kb, nt, split), shrink = shrink_us(a);
     // (the shrink splits a tile over up to 8 CTAs of 8 of its k-blocks)
     const int64_t before = ((int64_t)a.N / 128 + a.n_seg) * (n_kb < 8 ? 1 : (n_kb < 32 ? n_kb / 4 : 8));
-    if (ctas <= 240 && ctas + before <= 296)
-        return (base > shrink ? base + 0.25 * shrink : shrink + 0.25 * base) + finish;
-    return 0.75 * shrink + base + (double)((ctas + 239) / 240) * (1.5 + finish);
+    const double beside = 3 + (base > shrink ? base + 0.25 * shrink : shrink + 0.25 * base) + finish;
+    const double behind = 4.5 + 0.75 * shrink + base + (double)((ctas + 239) / 240) * finish;
+    const double crowd = ctas > 240 ? 1 : (double)(ctas + before - 296) / 148;
+    return crowd <= 0 ? beside : (crowd >= 1 ? behind : beside + crowd * (behind - beside));
 }
 
 // The few-token form that a model expects to be fastest, and its time.
