@@ -835,11 +835,15 @@ done:
 //
 // With adapters (LORA) the base does not wait for the shrink in front of it: what that kernel
 // waited for is all the base reads, so the product runs beside it, and only the finish waits
-// for V.  There the cluster's tokens are cut into groups of eight; a warp adds to 8 tokens x
-// 32 outputs the delta of each adapter among them, by mma.sync in registers (the adapter's B
-// rows and the tokens' V straight from L2; columns of other adapters' tokens are not taken
-// over, so that an infinity in B stays with its own tokens).  The delta is a few MFLOP: a
-// tcgen05 product would need B in shared memory and a TMEM round trip for it.
+// for V.  Complete when the shrink let this grid start means written to L2, no more: this SM's
+// L1 may hold lines that an earlier launch read (the scales of the call before, at the same
+// address), so whatever is read ahead of this grid's own wait -- scales, segments, the pool's
+// tables, B -- is read from L2 (__ldcg, TMA).  In the finish the cluster's tokens are cut into
+// groups of eight; a warp adds to 8 tokens x 32 outputs the delta of each adapter among them, by
+// mma.sync in registers (the adapter's B rows and the tokens' V straight from L2; columns of
+// other adapters' tokens are not taken over, so that an infinity in B stays with its own
+// tokens).  The delta is a few MFLOP: a tcgen05 product would need B in shared memory and a
+// TMEM round trip for it.
 constexpr int kFewThreads = 192;         // producer, MMA issuer, 4 warps that empty the accumulator
 constexpr int kFewLoraThreads = 256;     // and two more for the finish (two CTAs of 128 registers a thread fill an SM)
 
@@ -915,7 +919,7 @@ __device__ void few_tokens(const I8Args &a, FewTok *tok, int n0, int nv, int t0)
             int32_t r = 0;
             int64_t ao = 0, bo = 0;
             // (the shrink reports a bad one)
-            if (ad == -1 || !pool_adapter_ok(a.pool, ad, &r, &ao, &bo))
+            if (ad == -1 || !pool_adapter_ok<true>(a.pool, ad, &r, &ao, &bo))
                 tok[t] = {0, -1, 0};
             else
                 tok[t] = {bo, ad, r};
@@ -955,11 +959,11 @@ __device__ __forceinline__ void few_finish(const I8Args &p, const FewTok *tok, u
         few_load_b(p, tok[t + __ffs(left) - 1], o, 8 * q, b);
     float y[4][2] = {};
     if (o_ok) {
-        const float sw[4] = {p.Sw[o], p.Sw[o + 1], p.Sw[o + 2], p.Sw[o + 3]};
+        const float sw[4] = {__ldcg(p.Sw + o), __ldcg(p.Sw + o + 1), __ldcg(p.Sw + o + 2), __ldcg(p.Sw + o + 3)};
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             if (t + 2 * q + j < t_end) {
-                const float sx = p.Sx[n0 + t + 2 * q + j];
+                const float sx = __ldcg(p.Sx + n0 + t + 2 * q + j);
                 int4 v[8];
 #pragma unroll
                 for (int c = 0; c < 8; ++c)

@@ -74,16 +74,27 @@ struct PoolDev {
     int32_t n_adapters, max_rank, d_in, d_out;
 };
 
+// A read through L1, or from L2: the latter where the grid has not executed its own
+// griddepcontrol.wait yet, so that lines an earlier launch left in this SM's L1 do not count.
+template <bool L2, class T> __device__ __forceinline__ T ld_table(const T *p)
+{
+    if constexpr (L2)
+        return __ldcg(p);
+    else
+        return *p;
+}
+
 // Adapter a of pool P passes the device checks: id in range, rank a multiple of 8
 // in [8, max_rank], A and B offsets non-negative multiples of 8 whose matrices end
 // inside the pool.
+template <bool L2 = false>
 __device__ __forceinline__ bool pool_adapter_ok(const PoolDev &P, int32_t a, int32_t *r_out, int64_t *aoff,
                                                 int64_t *boff)
 {
     if (a < 0 || a >= P.n_adapters)
         return false;
-    const int32_t r = P.rank[a];
-    const int64_t ao = P.A_off[a], bo = P.B_off[a];
+    const int32_t r = ld_table<L2>(P.rank + a);
+    const int64_t ao = ld_table<L2>(P.A_off + a), bo = ld_table<L2>(P.B_off + a);
     if (r < 8 || r > P.max_rank || (r & 7))
         return false;
     if (ao < 0 || (ao & 7) || ao + (int64_t)r * P.d_in > P.A_elems)
