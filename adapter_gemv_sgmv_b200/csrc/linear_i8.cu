@@ -65,6 +65,12 @@ __device__ __forceinline__ void remote_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// (what this thread knows of shared memory comes with it: a waiter with CLUSTER sees it)
+__device__ __forceinline__ void remote_arrive_release(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // A box into this CTA's shared memory, completing on a barrier of the pair's leader.
 __device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y,
                                               uint64_t policy)
@@ -400,8 +406,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_
     unsigned char *sm = sm_dyn + ((1024 - (smem_u32(sm_dyn) & 1023)) & 1023);
     __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
     __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], f_full, f_empty, mma_drain, tab_full;
-    // a gather into a stage is asked for; the helpers' share of it is in
-    __shared__ __align__(8) uint64_t request_bar[LORA ? kStages : 1], gather_bar[LORA ? kStages : 1];
+    // a gather into a stage is asked for; it is in; (leader) the other CTA's is: its rows come by
+    // plain copies, which no byte count of full_bar stands for
+    __shared__ __align__(8) uint64_t request_bar[LORA ? kStages : 1], gather_bar[LORA ? kStages : 1],
+        peer_bar[LORA ? kStages : 1];
     __shared__ std::conditional_t<LORA, SegTable, int> tab;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -420,7 +428,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_
         if constexpr (LORA)
             for (int s = 0; s < kStages; ++s) {
                 mbar_init(&request_bar[s], 1);
-                mbar_init(&gather_bar[s], kHelp);
+                mbar_init(&gather_bar[s], 1 + kHelp);
+                mbar_init(&peer_bar[s], 1);
             }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
@@ -537,19 +546,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_
                         asm volatile("cp.async.wait_all;" ::: "memory");
                         fence_async_smem();
                         __syncwarp();
-                        if (!lead) {
-                            if (lane == 0)
-                                mbar_arrive(&gather_bar[s]);
-                        } else {
+                        if (lane == 0)
+                            mbar_arrive(&gather_bar[s]);
+                        if (lead)
                             alive = warp_wait(&gather_bar[s], (gathers >> s) & 1, &abort_flag, p.a.err, p.wait_ns);
-                        }
                         gathers ^= 1u << s;
                         if (!alive)
                             return;
                     }
                     if (lead && lane == 0) {
-                        // (the s V boxes leave after the gather is complete in both CTAs, so
-                        // the barrier, which waits for both, covers the gathered rows too)
+                        // (the leader's own gather is in before it arrives on full_bar)
                         const uint32_t b_bytes = with_b && !gather ? BN / 2 * w * 2 : 0;
                         if (rank == 0)
                             mbar_arrive_expect_tx(&full_bar[s], 2 * (kAtom + b_bytes));
@@ -589,7 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_
             const uint32_t idesc = idesc_i8(256, BN), idesc_f = idesc_bf16(256, BN);
             const uint64_t a0 = sw128_desc(smem_u32(sm)), b0 = sw128_desc(smem_u32(sm) + kAtom);
             int s = 0, t = 0, n_delta = 0;
-            uint32_t ph = 0;
+            uint32_t ph = 0, gathers = 0;            // bit s: parity of stage s's next gather
             bool alive = true;
             auto next = [&] {
                 if (++s == kStages) {
@@ -607,8 +613,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_
                 const RowMask mask(run.r0 - tile0, run.r1 - tile0);
                 int s_b = 0;                         // the stage that holds the B rows
                 for (int j = 0; j < run.kblocks() && wait(&full_bar[s], ph); ++j) {
-                    if ((j & 1) == 0)
+                    if ((j & 1) == 0) {
                         s_b = s;
+                        if (m < 0) {                 // gathered: the other CTA's half, too
+                            alive = mbar_wait<true>(&peer_bar[s], (gathers >> s) & 1, &abort_flag, p.a.err, p.wait_ns);
+                            if (!alive)
+                                return;
+                            tc_fence_after();
+                            gathers ^= 1u << s;
+                        }
+                    }
                     const uint32_t as = smem_u32(sm + s * kStage), bs = smem_u32(sm + s_b * kStage) + kAtom;
                     const int left = r - (j >> 1) * 64;
                     const int steps = ((left < 64 ? left : 64) + 15) >> 4;
@@ -659,6 +673,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::threads, 1) k_i8_
                     if (alive)
                         commit_pair(&f_full);
                 }
+            }
+        } else if (LORA && lane == 0 && !p.test_stall) {
+            // The other CTA's thread tells the leader of every gather here.  (By the producer, whose
+            // next loads then wait for the release, 2048 rows with 16 adapters of rank 24, 4096 ->
+            // 4096, take 56.4 us, and 55.2 so.)
+            uint32_t gathers = 0;
+            int s = 0;
+            bool alive = mbar_wait(&tab_full, 0, &abort_flag, p.a.err, p.wait_ns);
+            for (uint32_t u = c0; u < n_units && alive; u += G) {
+                const int tile0 = row_begin + pair_tile(u, n_pairs, n_ns).pair * 256;
+                s = (s + n_kb) % kStages;
+                for (Runs run(segs, tile0, min(tile0 + 256, row_end)); alive && run.next();)
+                    for (int j = 0; j < run.kblocks() && alive; ++j) {
+                        if ((j & 1) == 0 && run.ad.m < 0) {
+                            alive = mbar_wait(&gather_bar[s], (gathers >> s) & 1, &abort_flag, p.a.err, p.wait_ns);
+                            gathers ^= 1u << s;
+                            if (alive)
+                                remote_arrive_release(map_rank(smem_u32(&peer_bar[s]), 0));
+                        }
+                        if (++s == kStages)
+                            s = 0;
+                    }
             }
         }
         __syncwarp();

@@ -69,3 +69,41 @@ def test_adapted_scales_and_tables_rewritten_between_calls(N, d_in):
         check_rounded(widen(to_host(Ys[v])), wants[v], f"kind {v}")
         for i in range(v, rounds, kinds):
             assert torch.equal(Ys[i], Ys[v]), f"round {i} differs from round {v}"
+
+
+@pytest.mark.parametrize("d_out", [136, 1032])
+def test_gathered_adapter_rows_rewritten_between_calls(d_out):
+    """Behind 8192 rows pairs of CTAs run, in tiles of 128 outputs (136) and of 256 (1032).  B rows
+    of a rank without a tensor map, or off its grid, are gathered by both CTAs, each its half of
+    the tile, and one thread multiplies both halves: a half that came too late would leave the
+    round before's rows."""
+    rng = np.random.default_rng(d_out)
+    d_in, N, kinds, rounds = 64, 8193, 3, 18
+    hps = [rand_host_pool(rng, [24, 40, 120, 8, 104], d_in, d_out) for _ in range(kinds)]
+    pools = [DevPool(h) for h in hps]
+    pool = DevPool(hps[0])
+    cuts = np.sort(rng.choice(np.arange(1, N), 90, replace=False))
+    off = np.r_[0, cuts, N].astype(np.int32)
+    ads = (np.arange(91) % 5).astype(np.int32)
+    X = rand_x(rng, N, d_in)
+    x = dev_bf16(X)
+    Q, Sx = torch.empty(N, d_in, dtype=torch.int8, device=DEV), torch.empty(N, device=DEV)
+    Wq, Sw = torch.empty(d_out, d_in, dtype=torch.int8, device=DEV), torch.empty(d_out, device=DEV)
+    L.lora_quant_i8(x, Q, Sx)
+    L.lora_quant_i8(torch.randn(d_out, d_in, device=DEV) / d_in ** 0.5, Wq, Sw)
+    base = ((Q.double() @ Wq.double().t()) * Sx.double()[:, None] * Sw.double()).cpu().numpy()
+    seg_off, seg_ad = _i32(off), _i32(ads)
+    Ys = [torch.zeros(N, d_out, dtype=torch.bfloat16, device=DEV) for _ in range(rounds)]
+    torch.cuda.synchronize()
+    for i, Y in enumerate(Ys):
+        pool.B.copy_(pools[i % kinds].B)
+        pool.A.copy_(pools[i % kinds].A)
+        ws = L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, pool, seg_off, seg_ad, 0.5)
+    torch.cuda.synchronize()
+    assert L.lora_get_error(ws) == 0
+    for v in range(kinds):
+        want = base + oracle.linear_sgmv(X, np.zeros((d_out, d_in), np.uint16), hps[v], off, ads, 0.5)
+        check_parity(widen(to_host(Ys[v])), want, f"kind {v}")
+        check_rounded(widen(to_host(Ys[v])), want, f"kind {v}")
+        for i in range(v, rounds, kinds):
+            assert torch.equal(Ys[i], Ys[v]), f"round {i} differs from round {v}"
