@@ -2,6 +2,10 @@
 //
 //     v[n][j] = s sum_i A[a][j][i] x[n][i],   hi = bf16(v), lo = bf16(v - hi)
 //
+// At the end of the range: a finite v that bf16 would round to infinity has hi = bf16's largest
+// value (lo holds the rest), and where v is infinite or NaN so are both parts (inf - inf would
+// make a NaN of every infinity).
+//
 // A tile is at most 128 rows of one segment, its product [128 x d_in] x [d_in x rank].
 // Few tiles leave most SMs idle, and a single CTA takes d_in / 64 k-blocks in a row (44 us
 // for 23 segments of 1535 tokens at d_in 4096), so the reduction is split over the CTAs of
@@ -92,6 +96,18 @@ __device__ __forceinline__ Group find_tile(const SplitShrinkArgs &p, int tile, i
     g.cnt = __shfl_sync(0xffffffffu, g.cnt, owner & 31);
     g.item = __shfl_sync(0xffffffffu, g.item, owner & 31);
     return g;
+}
+
+// The parts of a value whose rounding to bf16 is no finite number (others' stay).
+constexpr float kBf16Max = 0x1.fep127f;
+__device__ __forceinline__ void end_of_range(float v, __nv_bfloat16 &hi, float &lo)
+{
+    if (!(fabsf(v) <= 3.402823466e38f)) {            // infinite or NaN
+        lo = v;
+    } else if (fabsf(__bfloat162float(hi)) > kBf16Max) {
+        hi = __float2bfloat16_rz(v);
+        lo = v - __bfloat162float(hi);
+    }
 }
 
 __global__ void __launch_bounds__(kVThreads) k_split_shrink(const __grid_constant__ SplitShrinkArgs p)
@@ -301,9 +317,14 @@ __global__ void __launch_bounds__(kVThreads) k_split_shrink(const __grid_constan
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
                 const float s0 = o * 8 + j < r ? p.scale * v[j] : 0.f, s1 = o * 8 + j + 1 < r ? p.scale * v[j + 1] : 0.f;
-                const __nv_bfloat162 h = __floats2bfloat162_rn(s0, s1);
+                __nv_bfloat162 h = __floats2bfloat162_rn(s0, s1);
                 const float2 back = __bfloat1622float2(h);
-                const __nv_bfloat162 l = __floats2bfloat162_rn(s0 - back.x, s1 - back.y);
+                float l0 = s0 - back.x, l1 = s1 - back.y;
+                if (!(fabsf(l0) <= kBf16Max && fabsf(l1) <= kBf16Max)) {
+                    end_of_range(s0, h.x, l0);
+                    end_of_range(s1, h.y, l1);
+                }
+                const __nv_bfloat162 l = __floats2bfloat162_rn(l0, l1);
                 hi[j / 2] = *reinterpret_cast<const uint32_t *>(&h);
                 lo[j / 2] = *reinterpret_cast<const uint32_t *>(&l);
             }
