@@ -9,9 +9,10 @@
 //
 // The angle is what needs care: at position 10^6 a frequency of 1 turns 160 000 times,
 // and fp32 would leave an error of several hundredths of a radian.  So the turns
-// u = pos * (freq / 2 pi) are formed and reduced to [-1/2, 1/2] in fp64, and only the
-// reduced angle goes to sincospif in fp32.  cos and sin carry m; the products are fp32,
-// each output is rounded to its type once.
+// u = pos * (freq / 2 pi) are formed and reduced to [-1/2, 1/2] in fp64, the factor in two
+// parts (one alone is off by up to 1.6 * 2^-53: 2e-6 of a radian at 2^31 turns), and only the
+// reduced angle goes to sincospif in fp32.  cos and sin carry m; the products are fp32, each
+// output is rounded to its type once.
 //
 // Bound: HBM, one read and one write per element.  A block takes up to 8 tokens: their
 // cos / sin come out once, in shared memory, for all heads, while the first loads of x
@@ -29,6 +30,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeHold = 2;        // items a thread has in flight
+constexpr double kInv2Pi = 0x1.45f306dc9c883p-3, kInv2PiLow = -0x1.6b01ec5417056p-57;    // 1 / 2 pi
 
 struct RopeMat {
     const void *x;
@@ -218,10 +220,11 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 5 : 4) k_rope(c
                 const int tt = i / p.half, j = i - tt * p.half;
                 const double at = p.pos64 ? (double)static_cast<const int64_t *>(p.pos)[n0 + tt]
                                           : (double)static_cast<const int32_t *>(p.pos)[n0 + tt];
-                // freq / 2 pi is off by 2^-53 of itself, the fma rounds once: at 2^31 positions
-                // of frequency 1 the angle is still within 2^-23
-                const double f = p.freq[j] * 0.15915494309189533577;
-                const double u = fma(at, f, -rint(at * f));
+                // f + fl = freq / 2 pi to 2^-104 of itself (the second constant is what the first
+                // leaves of 1 / 2 pi); at * f less its whole turns is exact but for one rounding
+                // below 1
+                const double f = p.freq[j] * kInv2Pi, fl = fma(p.freq[j], kInv2Pi, -f) + p.freq[j] * kInv2PiLow;
+                const double u = fma(at, fl, fma(at, f, -rint(at * f)));
                 float s, co;
                 sincospif(2.f * (float)u, &s, &co);
                 cs[i] = make_float2(co * p.m, s * p.m * p.sign);

@@ -337,18 +337,19 @@ LORA_API lora_status lora_linear_i8_sgmv(const int8_t *Q, int64_t ldq, const flo
  *   a' = mscale (a cos t - b sin t),   b' = mscale (b cos t + a sin t)
  * for j < rot/2; dimensions from rot to dim are copied.  `inverse` turns by -t
  * (times mscale): the gradient of the call with the same arguments.  The angle
- * is formed and reduced in fp64, the rotation is fp32, each output is rounded
- * once.
+ * is formed and reduced in fp64, rounded to fp32 as a share of a turn, the
+ * rotation is fp32, each output is rounded once.
  * mats: HOST array; x and y are device tensors of `dtype` with element strides
  * between tokens and between heads and unit stride inside a head.  y may be x
  * with the same strides (in place); otherwise no element of any y may overlap
  * any x or any other y.  x strides may be 0 (one token or head read for all);
  * y's tokens and heads must lie apart.  pos: device int32 or int64 [N]
- * (pos_bytes 4 or 8), any value, negative ones too (exact up to 2^31 turns of
- * a pair).  freq: device fp64 [rot/2], radians per position (lora_rope_freqs
- * fills them).  rot even, 2 <= rot <= dim <= LORA_MAX_ROPE_DIM; any odd sizes
- * and strides are taken, 16-byte accesses are used where sizes, strides and
- * addresses allow.  One launch, no workspace.
+ * (pos_bytes 4 or 8), any value, negative ones too; up to 2^31 turns of a pair
+ * and positions of 2^53 the reduced angle is the exact one, to fp32's rounding.
+ * freq: device fp64 [rot/2], radians per position (lora_rope_freqs fills them).
+ * rot even, 2 <= rot <= dim <= LORA_MAX_ROPE_DIM; any odd sizes and strides are
+ * taken, 16-byte accesses are used where sizes, strides and addresses allow.
+ * One launch, no workspace.
  */
 typedef struct lora_rope_mat {
     const void *x;
