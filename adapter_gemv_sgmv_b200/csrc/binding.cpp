@@ -126,12 +126,35 @@ Workspace read_workspace(PyObject *o)
     return w;
 }
 
+// A workspace that the caller made: its memory has to be the operands' device's (another
+// GPU's or the host's would be a bad address inside the kernels).
+void check_place(PyObject *given, const Workspace &w, int dev)
+{
+    PyObject *t = PyObject_GetAttrString(given, "tensor");
+    int at = -1;
+    if (t && THPVariable_Check(t)) {
+        const at::Tensor &v = THPVariable_Unpack(t);
+        at = v.is_cuda() ? v.get_device() : -1;
+    } else {                             // (some other object with ptr() and nbytes)
+        cudaPointerAttributes a = {};
+        if (cudaPointerGetAttributes(&a, w.at) != cudaSuccess)
+            cudaGetLastError();
+        else if (a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged)
+            at = a.device;
+    }
+    PyErr_Clear();
+    Py_XDECREF(t);
+    if (at != dev)
+        throw Refused{"the workspace must live on the tensors' device", LORA_ERR_INVALID_ARG};
+}
+
 // A new reference to the call's workspace: the one given, else this device and stream's;
 // under graph capture a fresh one from the graph's memory, so that no two graphs share it.
 Workspace workspace(PyObject *given, PyObject *stream, int dev, cudaStream_t s, size_t bytes)
 {
     if (given != Py_None) {
         Workspace w = read_workspace(given);
+        check_place(given, w, dev);
         Py_INCREF(given);
         return w;
     }
