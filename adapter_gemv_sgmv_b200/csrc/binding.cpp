@@ -38,6 +38,7 @@ struct Workspace {                      // the workspace of a device and stream,
     PyObject *object = nullptr;
     void *at = nullptr;
     size_t bytes = 0;
+    unsigned long long stream_id = 0;   // (a stream destroyed and a new one may have the same handle)
 };
 std::map<std::pair<int, cudaStream_t>, Workspace> g_workspaces;
 
@@ -148,6 +149,23 @@ void check_place(PyObject *given, const Workspace &w, int dev)
         throw Refused{"the workspace must live on the tensors' device", LORA_ERR_INVALID_ARG};
 }
 
+// Waits for all of the device's work, whatever its streams.
+void device_idle()
+{
+    // (a capture of another thread does not forbid it)
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    cudaError_t e = cudaSuccess;
+    Py_BEGIN_ALLOW_THREADS
+    e = cudaDeviceSynchronize();
+    Py_END_ALLOW_THREADS
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        throw Refused{"cudaDeviceSynchronize", LORA_ERR_CUDA};
+    }
+}
+
 // A new reference to the call's workspace: the one given, else this device and stream's;
 // under graph capture a fresh one from the graph's memory, so that no two graphs share it.
 Workspace workspace(PyObject *given, PyObject *stream, int dev, cudaStream_t s, size_t bytes)
@@ -164,8 +182,17 @@ Workspace workspace(PyObject *given, PyObject *stream, int dev, cudaStream_t s, 
         capturing = cudaStreamCaptureStatusNone;
     }
     const std::pair<int, cudaStream_t> key(dev, s);
+    unsigned long long id = 0;
     if (capturing == cudaStreamCaptureStatusNone) {
-        const auto it = g_workspaces.find(key);
+        if (cudaStreamGetId(s, &id) != cudaSuccess)
+            cudaGetLastError();
+        auto it = g_workspaces.find(key);
+        if (it != g_workspaces.end() && it->second.stream_id != id) {
+            device_idle();                   // the stream that used it is gone, its work may not be
+            it = g_workspaces.find(key);
+            if (it != g_workspaces.end())
+                it->second.stream_id = id;
+        }
         if (it != g_workspaces.end()) {
             if (it->second.bytes >= bytes) {
                 Py_INCREF(it->second.object);
@@ -189,6 +216,7 @@ Workspace workspace(PyObject *given, PyObject *stream, int dev, cudaStream_t s, 
         Workspace &kept = g_workspaces[key];
         PyObject *old = kept.object;
         kept = w;
+        kept.stream_id = id;
         Py_XDECREF(old);
     }
     return w;

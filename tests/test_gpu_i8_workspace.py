@@ -1,4 +1,7 @@
-"""Workspaces of the 8-bit projections: ones the caller made, in the wrong place."""
+"""Workspaces of the 8-bit projections: ones the caller made, in the wrong place; the library's
+own, of a stream whose handle another stream had before."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -74,3 +77,46 @@ def test_workspace_of_another_gpu_is_refused():
     Y = torch.ones((20, 32), dtype=torch.bfloat16, device=DEV)
     with pytest.raises(L.LoraError):
         L.lora_linear_i8(Q, Sx, Wq, Sw, Y, ws=L.Workspace(256, device="cuda:1"))
+
+
+def _cudart():
+    """The runtime that torch uses (its streams and this test's are of one kind)."""
+    for line in open("/proc/self/maps"):
+        if "libcudart.so" in line:
+            return ctypes.CDLL(line.split()[-1])
+    pytest.skip("torch's CUDA runtime is not a shared library")
+
+
+def test_streams_destroyed_with_work_in_flight():
+    """Streams made and destroyed one after another, each with calls queued when it goes: a new
+    stream may come at the handle of an old one, whose work still uses the workspace kept for it."""
+    rt = _cudart()
+    d_in, d_out, N = 1024, 1032, 600
+    pool = DevPool(rand_host_pool(np.random.default_rng(2), [64, 24], d_in, d_out))
+    sets = [_operands(N, d_in, d_out, seed) for seed in range(2)]
+    segs = [(_i32([0, 200, N]), _i32([0, 1])), (_i32([0, 450, N]), _i32([1, 0]))]
+    want = []
+    for (x, Q, Sx, Wq, Sw), (off, ad) in zip(sets, segs):
+        Y = torch.zeros(N, d_out, dtype=torch.bfloat16, device=DEV)
+        L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, pool, off, ad, 0.5)
+        want.append(Y)
+    torch.cuda.synchronize()
+    handles, done = [], []
+    for i in range(12):
+        h = ctypes.c_void_p()
+        assert rt.cudaStreamCreateWithFlags(ctypes.byref(h), 1) == 0
+        handles.append(h.value)
+        s = torch.cuda.ExternalStream(h.value)
+        (x, Q, Sx, Wq, Sw), (off, ad) = sets[i % 2], segs[i % 2]
+        Ys = [torch.zeros(N, d_out, dtype=torch.bfloat16, device=DEV) for _ in range(30)]
+        torch.cuda.current_stream().synchronize()
+        for Y in Ys:
+            ws = L.lora_linear_i8_sgmv(Q, Sx, x, Wq, Sw, Y, pool, off, ad, 0.5, stream=s)
+        done.append((i % 2, Ys, ws))
+        assert rt.cudaStreamDestroy(h) == 0
+    torch.cuda.synchronize()
+    for kind, Ys, ws in done:
+        assert L.lora_get_error(ws) == 0
+        for Y in Ys:
+            assert torch.equal(Y, want[kind])
+    print(f"{len(set(handles))} handles for {len(handles)} streams")
