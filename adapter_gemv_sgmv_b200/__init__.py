@@ -3,7 +3,7 @@
 The binding only marshals arguments (tensor pointers, sizes, the current CUDA
 stream) into the C ABI declared in include/lora_sgmv.h -- from Python with
 ctypes, or, for the short calls of an eager decode step, in a native module
-(csrc/binding.cpp, _native.so); every step of the computation runs in the
+(csrc/binding.cpp, _native-*.so); every step of the computation runs in the
 library's kernels.  There is no fallback: if the
 shared library is missing or cannot be loaded, every call raises LoraError.
 
@@ -412,7 +412,8 @@ def _native():
     if _native_module is None:
         lib = load()
         _torch()                                       # the module uses torch's libraries
-        path = os.path.join(_PKG, "_native.so")
+        from .build import native_path
+        path = native_path()
         if not os.path.exists(path):
             raise LoraError(f"{path} not found; build it with `python -m adapter_gemv_sgmv_b200.build`")
         spec = importlib.util.spec_from_file_location(__name__ + "._native", path)

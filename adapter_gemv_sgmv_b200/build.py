@@ -1,5 +1,6 @@
-"""Build liblora_sgmv.so in-tree with nvcc for sm_100a, and _native.so, the binding's
-native marshalling, against the installed torch.
+"""Build liblora_sgmv.so in-tree with nvcc for sm_100a, then the binding's native
+marshalling (_native-*.so) against the installed torch.  The library needs nvcc only:
+without torch, or with one without CUDA, the second step is left out.
 
     python -m adapter_gemv_sgmv_b200.build [--force]
 
@@ -10,6 +11,7 @@ when a call reaches the device.
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -21,7 +23,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblora_sgmv.so")
-EXT = os.path.join(PKG, "_native.so")
 EXT_SOURCE = os.path.join(CSRC, "binding.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -48,18 +49,26 @@ def stale() -> bool:
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
+def native_path() -> str:
+    """The native module of this interpreter and torch: another one of either has its own file."""
+    import torch
+    tag = f"{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(PKG, f"_native-{tag}.so")
+
+
 def build_native(force: bool = False, verbose: bool = False) -> str:
-    """The native half of the Python binding (host code only)."""
-    if not force and os.path.exists(EXT) and all(
-            os.path.getmtime(f) <= os.path.getmtime(EXT)
-            for f in [EXT_SOURCE, os.path.join(INCLUDE, "lora_sgmv.h")]):
-        return EXT
+    """The native half of the Python binding (host code only; needs torch with CUDA)."""
+    ext = native_path()
+    if not force and os.path.exists(ext) and all(
+            os.path.getmtime(f) <= os.path.getmtime(ext)
+            for f in [EXT_SOURCE, os.path.join(INCLUDE, "lora_sgmv.h"), os.path.abspath(__file__)]):
+        return ext
+    import torch
     from torch.utils import cpp_extension as ce
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     inc = [INCLUDE, sysconfig.get_paths()["include"], *ce.include_paths(), os.path.join(cuda, "include")]
     lib = [*ce.library_paths(), os.path.join(cuda, "lib64")]
-    import torch
-    tmp = EXT + f".tmp{os.getpid()}"
+    tmp = ext + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[f"-isystem{i}" for i in inc[1:]], "-I", inc[0], EXT_SOURCE, *[f"-L{d}" for d in lib],
@@ -68,12 +77,11 @@ def build_native(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
-    os.replace(tmp, EXT)
-    return EXT
+    os.replace(tmp, ext)
+    return ext
 
 
-def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    build_native(force, verbose)
+def build_library(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not stale():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
@@ -84,6 +92,23 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
+    return LIB
+
+
+def torch_with_cuda() -> bool:
+    if importlib.util.find_spec("torch") is None:
+        return False
+    import torch
+    return torch.version.cuda is not None
+
+
+def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    """The library, then (with torch) the native module, whose failure leaves the library made."""
+    build_library(force, verbose, extra)
+    if torch_with_cuda():
+        build_native(force, verbose)
+    elif verbose:
+        print("no torch with CUDA: the library alone (the Python binding's native module is left out)", flush=True)
     return LIB
 
 
