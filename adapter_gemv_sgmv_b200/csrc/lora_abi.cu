@@ -165,14 +165,21 @@ lora_status check_ws(void *ws, size_t ws_bytes, const Layout &L)
     return LORA_OK;
 }
 
+// Rows and widths that an 8-bit projection takes.
+bool i8_sizes_ok(int32_t N, int32_t d_in, int32_t d_out)
+{
+    return N >= 0 && N <= LORA_MAX_I8_ROWS && d_in > 0 && d_in <= LORA_MAX_I8_IN && !(d_in & 7) && d_out > 0 &&
+           d_out <= LORA_MAX_I8_ROWS && !(d_out & 7);
+}
+
 // The 8-bit operands of a projection: rows and addresses on 16-byte boundaries.
 lora_status check_i8(const int8_t *Q, int64_t ldq, const float *Sx, const int8_t *W, int64_t ldw, const float *Sw,
                      int32_t N, int32_t d_in, int32_t d_out)
 {
     if (N < 0 || d_in <= 0 || d_out <= 0 || (N > 0 && (!Q || !Sx)) || !W || !Sw || ldq < d_in || ldw < d_in)
         return LORA_ERR_INVALID_ARG;
-    if (N > LORA_MAX_I8_ROWS || d_out > LORA_MAX_I8_ROWS || d_in > LORA_MAX_I8_IN || (d_in & 7) || (d_out & 7) || (ldq & 15) || (ldw & 15) || misaligned(Q, 16) ||
-        misaligned(W, 16) || misaligned(Sx, 4) || misaligned(Sw, 4))
+    if (!i8_sizes_ok(N, d_in, d_out) || (ldq & 15) || (ldw & 15) || misaligned(Q, 16) || misaligned(W, 16) ||
+        misaligned(Sx, 4) || misaligned(Sw, 4))
         return LORA_ERR_UNSUPPORTED;
     return LORA_OK;
 }
@@ -319,10 +326,10 @@ size_t lora_workspace_size(int op, int32_t N, int32_t n_adapters, int32_t d_in, 
         return n_adapters >= 1 && n_adapters <= LORA_MAX_ADAPTERS && N == d_out
                    ? merge_workspace_size(d_in, d_out, max_rank) : 0;
     if (op == LORA_OP_LINEAR_I8)
-        return N >= 0 && d_in > 0 && d_in <= LORA_MAX_I8_IN && d_out > 0 ? sizeof(WsHeader) : 0;
+        return i8_sizes_ok(N, d_in, d_out) ? sizeof(WsHeader) : 0;
     if (op < LORA_OP_BGMV || op > LORA_OP_LINEAR_I8_SGMV || op == LORA_OP_MERGE)
         return 0;
-    if (op == LORA_OP_LINEAR_I8_SGMV && d_in > LORA_MAX_I8_IN)
+    if (op == LORA_OP_LINEAR_I8_SGMV && (!i8_sizes_ok(N, d_in, d_out) || (max_rank & 7)))
         return 0;
     Layout L;
     if (!layout(op, N, n_adapters, d_in, max_rank, n_items, max_ads_per_req, &L))
@@ -333,7 +340,7 @@ size_t lora_workspace_size(int op, int32_t N, int32_t n_adapters, int32_t d_in, 
 int lora_kernel_launches(int op, int32_t N, int32_t n_adapters, int32_t d_in, int32_t n_items)
 {
     if (op == LORA_OP_LINEAR_I8)
-        return N > 0 && d_in > 0 && d_in <= LORA_MAX_I8_IN ? 1 : 0;
+        return N > 0 && i8_sizes_ok(N, d_in, 8) ? 1 : 0;
     if (N <= 0 || n_adapters < 1 || n_adapters > LORA_MAX_ADAPTERS || d_in <= 0)
         return 0;
     switch (op) {
@@ -349,8 +356,9 @@ int lora_kernel_launches(int op, int32_t N, int32_t n_adapters, int32_t d_in, in
     case LORA_OP_MERGE:   // preparation + expand (tensor cores), or + plan + expand
         return tc_enabled() && N >= kTcGroup ? 2 : 3;
     case LORA_OP_LINEAR:  // plan + shrink + projection
-    case LORA_OP_LINEAR_I8_SGMV:
         return n_items > 0 ? 3 : 0;
+    case LORA_OP_LINEAR_I8_SGMV:
+        return n_items > 0 && i8_sizes_ok(N, d_in, 8) ? 3 : 0;
     default:
         return 0;
     }
