@@ -100,7 +100,10 @@ bool layout(int op, int32_t N, int32_t n_adapters, int32_t d_in, int32_t max_ran
         return false;
     const int64_t items = routed ? (int64_t)(N < n_adapters ? N : n_adapters) : n_items;
     memset(L, 0, sizeof *L);
-    L->max_groups = (int32_t)((int64_t)N / kGroup + items + 1);
+    const int64_t most_groups = (int64_t)N / kGroup + items + 1;
+    if (most_groups > INT32_MAX)
+        return false;
+    L->max_groups = (int32_t)most_groups;
     L->n_chunks = n_chunks_for(op, d_in);
     size_t off = 0;
     L->hdr = off;

@@ -1,5 +1,5 @@
 """Sizes that the 8-bit projections refuse have no workspace and no launches, as the header says
-of every operation."""
+of every operation; segment counts whose tiles no 32-bit number holds are refused."""
 import ctypes
 
 import pytest
@@ -46,3 +46,15 @@ def test_refused_sizes_have_no_workspace(lib, op, N, d_in, d_out, ok):
 def test_refused_ranks_have_no_workspace(lib, max_rank, ok):
     assert (_status(lib, L.OP_LINEAR_I8_SGMV, 4, 64, 32, max_rank) == WORKSPACE) == ok
     assert (L.lora_workspace_size(L.OP_LINEAR_I8_SGMV, 4, 4, 64, 32, max_rank, 2) > 0) == ok
+
+
+@pytest.mark.parametrize("op", [L.OP_SGMV_SHRINK, L.OP_SGMV_EXPAND, L.OP_LINEAR, L.OP_LINEAR_I8_SGMV])
+def test_more_segments_than_tiles_can_be_counted(lib, op):
+    """The largest counts: 2^31 - 1 tiles at N / 8 + n + 1."""
+    most = 2 ** 31 - 1 - 1000 // 8 - 1
+    assert L.lora_workspace_size(op, 1000, 4, 64, 32, 16, most) > 16 * most
+    assert L.lora_workspace_size(op, 1000, 4, 64, 32, 16, most + 1) == 0
+    assert L.lora_workspace_size(op, 1000, 4, 64, 32, 16, 2 ** 31 - 1) == 0
+    if op == L.OP_LINEAR_I8_SGMV:
+        assert _status(lib, op, 1000, 64, 32, n_seg=most) == WORKSPACE
+        assert _status(lib, op, 1000, 64, 32, n_seg=most + 1) == INVALID
