@@ -144,7 +144,8 @@ LORA_API size_t lora_workspace_size(int op, int32_t N, int32_t n_adapters, int32
  * function): lets a caller budget a CUDA graph or count launches.  0 for
  * arguments the entry point would reject or that launch nothing (N == 0), and
  * for LORA_OP_APPLY_PROJ, whose count depends on the pools (see
- * lora_sgmv_apply_proj). */
+ * lora_sgmv_apply_proj).  For LORA_OP_LINEAR_I8_SGMV the most that any number
+ * of segments takes, three: up to 128 segments a call launches two. */
 LORA_API int lora_kernel_launches(int op, int32_t N, int32_t n_adapters, int32_t d_in, int32_t n_items);
 
 /* Clear the workspace's error word (cudaMemsetAsync of its 256-byte header on
@@ -318,11 +319,14 @@ LORA_API lora_status lora_linear_i8(const int8_t *Q, int64_t ldq, const float *S
  *   Y[n][o] = Sx[n] Sw[o] sum_i Q[n][i] Wq[o][i] + scale * sum_{j < rank[a]} B[a][o][j] V[n][j],
  *   V[n][j] = sum_i A[a][j][i] X[n][i],
  * for seg_off[k] <= n < seg_off[k+1], a = seg_ad[k]; seg_ad[k] = -1: no delta.
- * The delta reads the tokens X (bf16) themselves, not their 8-bit form.  Rows
+ * The delta reads the tokens X (bf16) themselves, not their 8-bit form; scale *
+ * V is held in fp32 (beyond its range infinite), then as two bf16 parts, so an
+ * infinity in B leaves an infinity or a NaN in the outputs it meets.  Rows
  * outside every segment are not written.  Y is bf16, OUTPUT ONLY, rounded once.
  * Q, Sx, Wq, Sw as for lora_linear_i8; X, Y, pool, segments and device errors
  * as for lora_linear_sgmv.  Workspace: lora_workspace_size(LORA_OP_LINEAR_I8_SGMV,
- * N, n_adapters, d_in, d_out, max_rank, n_seg, 0).  Three launches.
+ * N, n_adapters, d_in, d_out, max_rank, n_seg, 0).  Two launches up to 128
+ * segments, three above.
  */
 LORA_API lora_status lora_linear_i8_sgmv(const int8_t *Q, int64_t ldq, const float *Sx, const void *X, int64_t ldx,
                               const int8_t *Wq, int64_t ldw, const float *Sw, void *Y, int64_t ldy,
