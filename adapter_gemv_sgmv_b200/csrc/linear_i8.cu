@@ -10,11 +10,13 @@
 // tile of 256 rows x BN outputs; each CTA holds 128 rows in its tensor memory and loads
 // 128 token rows and half of the tile's weight rows per 128-byte k-block, so a weight
 // byte crosses from L2 once per 256 rows and a token byte once per BN outputs.
-// Persistent, 320 threads a CTA:
-//   warp 0     producer: TMA boxes into a ring; both CTAs' boxes complete on the
-//              leader's barrier;
-//   warp 1     (leader) one thread issues tcgen05.mma kind::i8 (M = 256, K = 32);
-//   warps 2-9  epilogue: tensor memory -> scale -> y.
+// Persistent, 320 threads a CTA, with adapters 640:
+//   warp 0        producer: TMA boxes into a ring; both CTAs' boxes complete on the
+//                 leader's barrier;
+//   warp 1        (leader) one thread issues tcgen05.mma kind::i8 (M = 256, K = 32);
+//                 (other CTA, with adapters) tells the leader of the B rows gathered there;
+//   warps 2-9     epilogue: tensor memory -> scale -> y (with adapters warps 2-17);
+//   warps 18, 19  (with adapters) share the producer's gathers of B rows.
 // Without adapters two integer accumulators alternate, so a tile's epilogue runs under
 // the next one's products.  The delta (LORA) takes the second half of tensor memory as an
 // fp32 accumulator: bf16 k-blocks of (s v) high and low parts against the adapter's B
@@ -22,6 +24,10 @@
 // run and hands their accumulator to the next tile, then the fp32 sums while that one
 // starts.  (160 columns, which leave room for two integer accumulators beside the fp32
 // one, were slower: a tile of 256 x BN reads (256 + BN) / (256 BN) bytes a product.)
+// B rows of a rank with a tensor map come by TMA.  Others are gathered, 16 bytes at a time, by
+// the producer and two helpers: request_bar[s] lets the helpers into stage s, gather_bar[s] says
+// that all three are done (the producer then sends the box of s V, whose barrier the leader's MMA
+// thread waits for), and the other CTA's share reaches that thread through peer_bar[s].
 // A tile's rows may belong to different adapters.  Each run of rows with one adapter has
 // k-blocks of its own, multiplied with every other row of the accumulator masked: a row
 // must not meet another adapter's B even with factors of zero, for that B may hold an
@@ -940,7 +946,7 @@ __device__ __forceinline__ int ld_remote(uint32_t addr)
 
 // The adapter of each of the tile's tokens and the scales of its tokens and outputs, by the four
 // warps that empty the accumulator.  (Read from L2 by every finishing warp, the scales cost 256
-// tokens in 16 segments, 4096 -> 4096, 25.7 us for 24.)
+// tokens in 16 segments, 4096 -> 4096, 25.7 us for 24.3.)
 __device__ void few_tokens(const I8Args &a, FewTok *tok, FewScales &sc, int n0, int nv, int o0, int t0)
 {
     for (int t = t0; t < nv; t += 128) {
@@ -1395,10 +1401,11 @@ double few_us(const I8Args &a, int n_kb, int nt, int split)
 //   tiles of 128 outputs.
 // * Few tokens multiply beside it where the CTAs of both find room, then finish in rounds of
 //   eight warps: 1.1 a round, and 0.9 (ranks over 64: 1.1) for each adapter among eight tokens.
-// Measured (us, pairs / few): 16 tokens in 4 segments, 4096 -> 4096 29 / 13.0, 14336 -> 4096
-// 62 / 20.4; 256 in 16, 4096 -> 4096 38 / 24.0; 1024 in 16, 4096 -> 1024 34.4 / 23.4; 560 in
+// Measured (us, pairs / few): 16 tokens in 4 segments, 4096 -> 4096 29 / 13.3, 14336 -> 4096
+// 62 / 20.3; 256 in 16, 4096 -> 4096 38 / 24.5; 1024 in 16, 4096 -> 1024 34.4 / 23.6; 560 in
 // 10, 8496 -> 6632 79 / 103; 1706 in 24, 3336 -> 3560 74 / 110.  Over 112 random shapes of 16
-// to 2900 tokens the choice takes 2 % longer than the better of all.
+// to 2900 tokens the choice takes 2 % longer than the best of the forms that best_few() admits
+// (tiles narrower than the tokens, which it does not, were not timed).
 double shrink_us(const I8Args &a)
 {
     return 6 + a.d_in / 1500.0;
@@ -1445,7 +1452,8 @@ FewChoice best_few(const I8Args &a, int n_kb, int max_nt, double (*model)(const 
 {
     FewChoice best = {0, 1, 1e30};
     for (int nt : {16, 32, 64, 128, 256}) {
-        // (narrow tiles would read the weight again and again; the model ends at some thousand tokens)
+        // (narrow tiles would read a large weight again and again -- over a small one, which they
+        // would spread over more SMs, they are not measured; the model ends at some thousand tokens)
         if ((nt < 128 && nt < a.N) || nt > max_nt || a.N > 8192)
             continue;
         for (int split = 1; split <= 8 && (split == 1 || 2 * split <= n_kb); split *= 2) {
